@@ -85,6 +85,12 @@ typedef enum {
     KLA_ERR_TOO_LARGE = 7            /* problem exceeds the static scratch of kla_scan_forward_static */
 } kla_status_t;
 
+/* How the gates of kla_gated_scan_* are laid out. */
+typedef enum {
+    KLA_GATE_CHANNEL = 0, /* one gate per channel: f is [B, T, H, N] */
+    KLA_GATE_HEAD = 1     /* one gate per head, shared by its N channels: f is [B, T, H] */
+} kla_gate_t;
+
 /* ABI version of the loaded library (KLA_ABI_VERSION it was built with). */
 int kla_abi_version(void);
 
@@ -496,6 +502,84 @@ kla_status_t kla_scan_forward_lti(const float *a, const void *phi, const void *b
  */
 kla_status_t kla_scan_forward_lti_plan(int64_t B, int64_t T, int64_t H, int64_t N, kla_dtype_t in_dtype,
                                        const void *phi, const void *b, int *kernel, int *launches);
+
+/*
+ * The gated linear recurrence with given gates, over whole sequences:
+ *
+ *   h_t = f_t h_{t-1} + x_t          (h_{-1} = h0)
+ *
+ * for every channel (b, h, n) independently -- the affine recursion of the
+ * filter's information mean with a gate that the caller forms (a decay, a
+ * forget gate) instead of the precision ratio.
+ *
+ *   f   gates, dtype in_dtype (read only): [B, T, H, N], or [B, T, H] shared
+ *       by the channels of a head (`gate`)
+ *   x   [B, T, H, N] inputs, dtype in_dtype (read only)
+ *   h0  [B, H, N] fp32 entering state (read only), or NULL for zero
+ *   h   [B, T, H, N] fp32 states (written); the last row is the state to
+ *       continue from with kla_gated_scan_step
+ *
+ * Any real gate is allowed, 0 (the state starts afresh: sequences packed one
+ * after another) and negative ones among them.  The magnitude of the product
+ * of the gates of any 256 consecutive tokens must stay below 2^127 (it can
+ * exceed that only where gates are above 1), and the states within fp32
+ * range; an input that is not finite makes the states from its token on
+ * undefined, in its channel only.  States and arithmetic are fp32.  Any size
+ * and alignment; no workspace, one kernel launch, the same bits from run to
+ * run.  T == 0 or B*H*N == 0 is a valid empty problem.  h may not overlap the
+ * inputs.
+ */
+kla_status_t kla_gated_scan_forward(const void *f, const void *x, kla_dtype_t in_dtype, kla_gate_t gate,
+                                    const float *h0, float *h, int64_t B, int64_t T, int64_t H, int64_t N,
+                                    void *stream);
+
+/*
+ * One decode token of it: h_out = f h + x.
+ *
+ *   f      [B, H, N] or [B, H] (`gate`), x [B, H, N], dtype in_dtype
+ *   h      [B, H, N] fp32 state before the token
+ *   h_out  [B, H, N] fp32 state after it: h itself (in place), or an array
+ *          that does not overlap it (the old state is kept)
+ */
+kla_status_t kla_gated_scan_step(const void *f, const void *x, kla_dtype_t in_dtype, kla_gate_t gate,
+                                 const float *h, float *h_out, int64_t B, int64_t H, int64_t N, void *stream);
+
+/*
+ * Device workspace that kla_gated_scan_backward needs when grad_f is wanted,
+ * written to *bytes: 0 but for gates shared by a head of more than 32
+ * channels (a partial sum per token, head and 32 channels).
+ */
+kla_status_t kla_gated_scan_backward_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N,
+                                                    kla_dtype_t in_dtype, kla_gate_t gate, size_t *bytes);
+
+/*
+ * Gradients of a scalar loss through kla_gated_scan_forward:
+ *
+ *   E_t = g_t + f_{t+1} E_{t+1}      (a reverse-time scan; E_T = 0)
+ *   d/d x_t = E_t,  d/d f_t = E_t h_{t-1},  d/d h0 = f_0 E_0,
+ *
+ * with d/d f_t summed over the N channels that share the gate (KLA_GATE_HEAD;
+ * in a fixed order, the same bits from run to run).
+ *
+ *   f, h0      as in the forward call; h its output (needed for grad_f only)
+ *   g_h        [B, T, H, N] fp32 gradient with respect to the states; that of
+ *              the last state is its last row
+ *   grad_f     gradient of f, in its shape and in_dtype, or NULL
+ *   grad_x     [B, T, H, N] in in_dtype, or NULL
+ *   grad_h0    [B, H, N] fp32, or NULL
+ *   workspace  at least kla_gated_scan_backward_workspace_size(...) bytes,
+ *              256-byte aligned (NULL when that is 0 or grad_f is NULL);
+ *              contents on entry do not matter.  Concurrent calls need their
+ *              own.
+ *
+ * fp32 arithmetic; grad_f and grad_x are rounded once, on store.  B*H*N == 0
+ * is a valid empty problem; T == 0 writes a zero grad_h0.  Outputs must not
+ * overlap inputs, the workspace or each other.
+ */
+kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype, kla_gate_t gate, const float *h0,
+                                     const float *h, const float *g_h, void *grad_f, void *grad_x,
+                                     float *grad_h0, int64_t B, int64_t T, int64_t H, int64_t N,
+                                     void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Synchronise `stream`, then report the first failure since the previous

@@ -14,6 +14,8 @@ _API_NAMES = {
     "scan_backward", "backward_workspace_size", "backward_plan", "debug_force_backward_kernel",
     "KalmanFilterScan", "kalman_filter", "layer_forward", "layer_workspace_size", "layer_step",
     "attention_weights", "scan_forward_lti", "lti_workspace_size", "lti_plan",
+    "gated_scan_forward", "gated_scan_step", "gated_scan_backward", "gated_scan_backward_workspace_size",
+    "GatedScan", "gated_scan",
 }
 
 

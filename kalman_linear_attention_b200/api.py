@@ -24,6 +24,7 @@ STATUS = {0: "KLA_OK", 1: "KLA_ERR_INVALID_ARG", 2: "KLA_ERR_UNSUPPORTED_DTYPE",
 KLA_OK, KLA_ERR_INVALID_ARG, KLA_ERR_UNSUPPORTED_DTYPE = 0, 1, 2
 KLA_ERR_WORKSPACE_TOO_SMALL, KLA_ERR_CUDA, KLA_ERR_TIMEOUT, KLA_ERR_MISALIGNED = 3, 4, 5, 6
 KLA_ERR_TOO_LARGE = 7
+KLA_GATE_CHANNEL, KLA_GATE_HEAD = 0, 1
 STATIC_SCRATCH_BYTES = 32 << 20  # KLA_STATIC_SCRATCH_BYTES
 
 # Every exported symbol of include/kla.h, with (restype, argtypes).
@@ -72,6 +73,13 @@ SIGNATURES = {
                                             _I64, _I64, _I64, _I64, _VP, _SZ, _VP]),
     "kla_scan_forward_lti_plan": (ctypes.c_int, [_I64, _I64, _I64, _I64, ctypes.c_int, _VP, _VP,
                                                  ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
+    "kla_gated_scan_forward": (ctypes.c_int, [_VP, _VP, ctypes.c_int, ctypes.c_int, _VP, _VP, _I64, _I64, _I64,
+                                              _I64, _VP]),
+    "kla_gated_scan_step": (ctypes.c_int, [_VP, _VP, ctypes.c_int, ctypes.c_int, _VP, _VP, _I64, _I64, _I64, _VP]),
+    "kla_gated_scan_backward_workspace_size": (ctypes.c_int, [_I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int,
+                                                              ctypes.POINTER(_SZ)]),
+    "kla_gated_scan_backward": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.c_int, _VP, _VP, _VP, _VP, _VP, _VP, _I64,
+                                               _I64, _I64, _I64, _VP, _SZ, _VP]),
 }
 ATTENTION_MAX_WINDOW = 64  # KLA_ATTENTION_MAX_WINDOW
 
@@ -600,3 +608,180 @@ def scan_forward_lti(a: torch.Tensor, phi: torch.Tensor, b: torch.Tensor, lam0: 
                                         _ptr(workspace), workspace.numel(), _stream_handle(stream))
     _check(st, "kla_scan_forward_lti")
     return tuple(outs)
+
+
+# ------------------------------------------------ gated linear recurrence
+class _Launch:
+    """Device, stream and allocations of one call: the work goes to ``stream``
+    (default: the current stream of the tensors' device), and what the call
+    allocates belongs to that stream, whichever one is current."""
+
+    def __init__(self, like: torch.Tensor, stream: Optional[torch.cuda.Stream]):
+        self.device = like.device
+        index = like.device.index
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {like.device}")
+        current = torch.cuda.current_stream(index)
+        self.handle = current.cuda_stream if stream is None else stream.cuda_stream
+        self._outer = None
+        if torch.cuda.current_device() != index or self.handle != current.cuda_stream:
+            self._outer = torch.cuda.stream(stream if stream is not None else current)
+
+    def __enter__(self) -> "_Launch":
+        if self._outer is not None:
+            self._outer.__enter__()
+        return self
+
+    def __exit__(self, *exc) -> None:
+        if self._outer is not None:
+            self._outer.__exit__(*exc)
+
+    def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def _require_like(device: torch.device, **tensors: Optional[torch.Tensor]) -> None:
+    """Every tensor dense and on `device`, a CUDA device."""
+    if device.type != "cuda":
+        raise ValueError("tensor must be on a CUDA device")
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, as the other tensors are")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _require_shape(name: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype) -> None:
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _gate(f: torch.Tensor, shape) -> int:
+    """The gate layout of f for states of `shape` ([.., H, N])."""
+    if f.shape == shape:
+        return KLA_GATE_CHANNEL
+    if f.shape == shape[:-1]:
+        return KLA_GATE_HEAD
+    raise ValueError(f"f must be {list(shape)} (a gate per channel) or {list(shape[:-1])} (shared by a head), "
+                     f"got {list(f.shape)}")
+
+
+def gated_scan_forward(f: torch.Tensor, x: torch.Tensor, h0: Optional[torch.Tensor] = None, *,
+                       out: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The gated linear recurrence h_t = f_t h_{t-1} + x_t
+    (kla_gated_scan_forward): x [B, T, H, N]; f of the same shape, or
+    [B, T, H] with one gate for a head's channels (both fp32 or both bf16); h0
+    [B, H, N] fp32 (None: zero).  Returns the states, fp32 [B, T, H, N]; the
+    last one continues with gated_scan_step.  Enqueued on ``stream`` (default:
+    the current stream) without synchronising."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B, T, H, N]")
+    B, T, H, N = x.shape
+    gate = _gate(f, x.shape)
+    code = _dtype_code(x)
+    if f.dtype != x.dtype:
+        raise TypeError("f and x must share one dtype")
+    _require_shape("h0", h0, (B, H, N), torch.float32)
+    _require_shape("out", out, x.shape, torch.float32)
+    _require_like(x.device, f=f, x=x, h0=h0, out=out)
+    with _Launch(x, stream) as on:
+        if out is None:
+            out = on.empty(x.shape, torch.float32)
+        st = lib().kla_gated_scan_forward(_ptr(f), _ptr(x), code, gate, _ptr(h0), _ptr(out), B, T, H, N, on.handle)
+    _check(st, "kla_gated_scan_forward")
+    return out
+
+
+def gated_scan_step(f: torch.Tensor, x: torch.Tensor, h_state: torch.Tensor, *,
+                    out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One decode token of the gated recurrence (kla_gated_scan_step): x
+    [B, H, N], f of that shape or [B, H], h_state [B, H, N] fp32.  The new state
+    goes to ``out``, or in place to h_state without it; returns where it went."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, H, N]")
+    B, H, N = x.shape
+    gate = _gate(f, x.shape)
+    code = _dtype_code(x)
+    if f.dtype != x.dtype:
+        raise TypeError("f and x must share one dtype")
+    if out is None:
+        out = h_state
+    _require_shape("h_state", h_state, x.shape, torch.float32)
+    _require_shape("out", out, x.shape, torch.float32)
+    _require_like(x.device, f=f, x=x, h_state=h_state, out=out)
+    with _Launch(x, stream) as on:
+        st = lib().kla_gated_scan_step(_ptr(f), _ptr(x), code, gate, _ptr(h_state), _ptr(out), B, H, N, on.handle)
+    _check(st, "kla_gated_scan_step")
+    return out
+
+
+def gated_scan_backward_workspace_size(B: int, T: int, H: int, N: int, dtype: torch.dtype = torch.float32,
+                                       head_gate: bool = False) -> int:
+    code = KLA_BF16 if dtype == torch.bfloat16 else KLA_F32
+    out = ctypes.c_size_t(0)
+    _check(lib().kla_gated_scan_backward_workspace_size(B, T, H, N, code, int(head_gate), ctypes.byref(out)),
+           "kla_gated_scan_backward_workspace_size")
+    return int(out.value)
+
+
+def gated_scan_backward(f: torch.Tensor, h: torch.Tensor, g_h: torch.Tensor, h0: Optional[torch.Tensor] = None, *,
+                        want: Sequence[bool] = (True, True, True),
+                        workspace: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> Tuple[Optional[torch.Tensor], ...]:
+    """Gradients through gated_scan_forward (kla_gated_scan_backward): f and
+    h0 as given to it, h the states it returned, g_h the loss gradient with
+    respect to them (fp32).  Returns the gradients with respect to (f, x, h0):
+    the first two in f's dtype, the last fp32; None where ``want`` is False."""
+    if h.dim() != 4:
+        raise ValueError("h must be the forward output, [B, T, H, N]")
+    B, T, H, N = h.shape
+    gate = _gate(f, h.shape)
+    code = _dtype_code(f)
+    _require_shape("h", h, h.shape, torch.float32)
+    _require_shape("g_h", g_h, h.shape, torch.float32)
+    _require_shape("h0", h0, (B, H, N), torch.float32)
+    _require_like(h.device, f=f, h=h, g_h=g_h, h0=h0, workspace=workspace)
+    with _Launch(h, stream) as on:
+        gf = on.empty(f.shape, f.dtype) if want[0] else None
+        gx = on.empty(h.shape, f.dtype) if want[1] else None
+        gh0 = on.empty((B, H, N), torch.float32) if want[2] else None
+        if workspace is None and gate == KLA_GATE_HEAD and want[0]:
+            n = gated_scan_backward_workspace_size(B, T, H, N, f.dtype, True)
+            workspace = on.empty(n, torch.uint8) if n else None
+        st = lib().kla_gated_scan_backward(
+            _ptr(f), code, gate, _ptr(h0), _ptr(h), _ptr(g_h), _ptr(gf), _ptr(gx), _ptr(gh0), B, T, H, N,
+            _ptr(workspace), workspace.numel() if workspace is not None else 0, on.handle)
+    _check(st, "kla_gated_scan_backward")
+    return gf, gx, gh0
+
+
+class GatedScan(torch.autograd.Function):
+    """Differentiable gated recurrence: forward = kla_gated_scan_forward,
+    backward = kla_gated_scan_backward.  Inputs (f, x, h0) as in
+    gated_scan_forward; returns the states."""
+
+    @staticmethod
+    def forward(ctx, f, x, h0):
+        h = gated_scan_forward(f, x, h0)
+        ctx.save_for_backward(f, h, h0)
+        return h
+
+    @staticmethod
+    def backward(ctx, g_h):
+        f, h, h0 = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        return gated_scan_backward(f, h, g_h.contiguous(), h0, want=(need[0], need[1], need[2] and h0 is not None))
+
+
+def gated_scan(f: torch.Tensor, x: torch.Tensor, h0: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The states of the gated recurrence, differentiable with respect to
+    f, x and h0 through the CUDA backward scan."""
+    return GatedScan.apply(f, x, h0)

@@ -1,0 +1,294 @@
+// kla_gated.cu -- host side of the gated linear recurrence (kla_gated_scan_*
+// of include/kla.h): argument checks, tiling and launches of the kernels in
+// kla_gated.cuh.
+#include "kla_gated.cuh"
+
+#include <algorithm>
+
+namespace {
+
+using namespace kla_mixer;
+
+bool gate_ok(kla_gate_t g) { return g == KLA_GATE_CHANNEL || g == KLA_GATE_HEAD; }
+
+struct Sizes {
+    int64_t HN = 0, C = 0, rows = 0, n = 0;  // H*N, B*H*N, B*T*H, B*T*H*N
+    int64_t gates = 0;                       // elements of f
+};
+bool sizes(int64_t B, int64_t T, int64_t H, int64_t N, kla_gate_t gate, Sizes *s) {
+    int64_t bt = 0, bytes = 0;
+    if (T < 0 || !mul_ok(H, N, &s->HN) || !mul_ok(B, s->HN, &s->C) || !mul_ok(B, T, &bt) ||
+        !mul_ok(bt, H, &s->rows) || !mul_ok(bt, s->HN, &s->n) || !mul_ok(s->n, 4, &bytes) ||
+        !mul_ok(s->rows, 4, &bytes))
+        return false;
+    s->gates = gate == KLA_GATE_HEAD ? s->rows : s->n;
+    return true;
+}
+
+// Tokens per warp and round.
+#ifndef KLA_GATED_L
+#define KLA_GATED_L 16
+#endif
+#ifndef KLA_GATED_BACKWARD_L
+#define KLA_GATED_BACKWARD_L 16
+#endif
+// Clusters are doubled while the CTAs are fewer than this many per SM.
+#ifndef KLA_GATED_FILL
+#define KLA_GATED_FILL 2
+#endif
+#ifndef KLA_GATED_VEC_F32
+#define KLA_GATED_VEC_F32 1
+#endif
+#ifndef KLA_GATED_VEC_BF16
+#define KLA_GATED_VEC_BF16 2
+#endif
+
+struct Launch {
+    GatedTiles g;
+    int64_t tiles;
+    int W, C, group;
+};
+
+// Tiles of 32 x VEC channels.  Tiles run on over the heads of a batch row,
+// unless a gate is shared by a head whose channels and a tile's do not divide
+// one another: then each head has tiles of its own, so that the sum over its
+// channels stays within whole tiles.
+Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, bool head, int vec, int L) {
+    Launch l;
+    const int64_t cw = 32 * vec;
+    const bool own = head && N % cw != 0 && cw % N != 0;
+    l.g.T = T; l.g.H = H; l.g.N = N; l.g.HN = H * N;
+    l.g.seg = own ? N : H * N;
+    l.g.per_seg = (l.g.seg + cw - 1) / cw;
+    l.g.per_row = l.g.per_seg * (own ? H : 1);
+    l.tiles = B * l.g.per_row;
+    l.group = head && !own && N < cw ? (int)(N / vec) : 32;
+    l.W = (int)std::min<int64_t>(kGatedMaxWarps, (T + L - 1) / L);
+    l.C = 1;
+    while (l.C < kGatedMaxCluster && l.tiles * l.C < (int64_t)KLA_GATED_FILL * sm_count() &&
+           (int64_t)l.C * l.W * L < T)
+        l.C *= 2;
+    return l;
+}
+
+// Tiles of a head whose gate gradients are added up by the reduce kernel.
+int64_t parts_of(int64_t N, int vec) { return (N + 32 * vec - 1) / (32 * vec); }
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int cluster, cudaStream_t stream, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+template <typename Tin, int VEC, bool HEAD>
+cudaError_t run_forward(const Launch &l, const GatedParams &prm, cudaStream_t st) {
+    constexpr int L = KLA_GATED_L;
+    return l.C > 1 ? launch(kla_gated_forward_kernel<Tin, VEC, HEAD, L, true>, l.tiles * l.C, 32 * l.W, l.C, st, prm)
+                   : launch(kla_gated_forward_kernel<Tin, VEC, HEAD, L, false>, l.tiles, 32 * l.W, 1, st, prm);
+}
+
+template <typename Tin, int VEC, bool HEAD>
+cudaError_t run_backward(const Launch &l, const GatedBackwardParams &prm, cudaStream_t st) {
+    constexpr int L = KLA_GATED_BACKWARD_L;
+    return l.C > 1 ? launch(kla_gated_backward_kernel<Tin, VEC, HEAD, L, true>, l.tiles * l.C, 32 * l.W, l.C, st, prm)
+                   : launch(kla_gated_backward_kernel<Tin, VEC, HEAD, L, false>, l.tiles, 32 * l.W, 1, st, prm);
+}
+
+// Channels per lane: as the type's constant says where every row of the
+// arrays (pointers `p`, of element sizes `e`; null ones are not used) starts
+// on a vector, else one.
+int vec_of(kla_dtype_t dt, int64_t HN, int64_t N, bool head, const void *const *p, const int64_t *e, int n) {
+    const int vec = dt == KLA_F32 ? KLA_GATED_VEC_F32 : KLA_GATED_VEC_BF16;
+    if (HN % vec != 0 || (head && N % vec != 0)) return 1;
+    for (int i = 0; i < n; ++i)
+        if (p[i] && !aligned(p[i], vec * e[i])) return 1;
+    return vec;
+}
+
+template <typename Tin>
+int step_vec(const GatedStepParams &prm, bool head) {
+    const int64_t e = (int64_t)sizeof(Tin);
+    const bool ok = prm.C % 4 == 0 && (!head || prm.N % 4 == 0) && (head || aligned(prm.f, 4 * e)) &&
+                    aligned(prm.x, 4 * e) && aligned(prm.h, 16) && aligned(prm.out, 16);
+    return ok ? 4 : 1;
+}
+
+template <typename Tin>
+cudaError_t run_step(const GatedStepParams &prm, bool head, cudaStream_t st) {
+    const int vec = step_vec<Tin>(prm, head);
+    const int64_t work = (prm.C + vec - 1) / vec;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>((work + 255) / 256, (int64_t)sm_count() * 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (vec == 4)
+        return head ? cudaLaunchKernelEx(&cfg, kla_gated_step_kernel<Tin, 4, true>, prm)
+                    : cudaLaunchKernelEx(&cfg, kla_gated_step_kernel<Tin, 4, false>, prm);
+    return head ? cudaLaunchKernelEx(&cfg, kla_gated_step_kernel<Tin, 1, true>, prm)
+                : cudaLaunchKernelEx(&cfg, kla_gated_step_kernel<Tin, 1, false>, prm);
+}
+
+}  // namespace
+
+KLA_API kla_status_t kla_gated_scan_forward(const void *f, const void *x, kla_dtype_t in_dtype, kla_gate_t gate,
+                                            const float *h0, float *h, int64_t B, int64_t T, int64_t H, int64_t N,
+                                            void *stream) {
+    if (B < 0 || T < 0 || H < 0 || N < 0 || !gate_ok(gate)) return KLA_ERR_INVALID_ARG;
+    if (!dtype_ok(in_dtype)) return KLA_ERR_UNSUPPORTED_DTYPE;
+    Sizes s;
+    if (!sizes(B, T, H, N, gate, &s)) return KLA_ERR_INVALID_ARG;
+    if (s.n == 0) return KLA_OK;
+    if (!f || !x || !h) return KLA_ERR_INVALID_ARG;
+    const int64_t e = dtype_size(in_dtype);
+    const Range outs[1] = {range_of(h, 4 * s.n)};
+    const Range ins[3] = {range_of(f, e * s.gates), range_of(x, e * s.n), range_of(h0, 4 * s.C)};
+    if (any_overlap(outs, 1, ins, 3)) return KLA_ERR_INVALID_ARG;
+
+    const bool head = gate == KLA_GATE_HEAD;
+    const void *p[3] = {head ? nullptr : f, x, h};
+    const int64_t es[3] = {e, e, 4};
+    const int vec = vec_of(in_dtype, s.HN, N, head, p, es, 3);
+    const Launch l = plan(B, T, H, N, head, vec, KLA_GATED_L);
+    if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
+    GatedParams prm;
+    prm.g = l.g;
+    prm.f = f; prm.x = x; prm.h0 = h0; prm.h = h;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t err;
+    if (in_dtype == KLA_F32) {
+        if (vec == 1)
+            err = head ? run_forward<float, 1, true>(l, prm, st) : run_forward<float, 1, false>(l, prm, st);
+        else
+            err = head ? run_forward<float, KLA_GATED_VEC_F32, true>(l, prm, st)
+                       : run_forward<float, KLA_GATED_VEC_F32, false>(l, prm, st);
+    } else {
+        if (vec == 1)
+            err = head ? run_forward<__nv_bfloat16, 1, true>(l, prm, st)
+                       : run_forward<__nv_bfloat16, 1, false>(l, prm, st);
+        else
+            err = head ? run_forward<__nv_bfloat16, KLA_GATED_VEC_BF16, true>(l, prm, st)
+                       : run_forward<__nv_bfloat16, KLA_GATED_VEC_BF16, false>(l, prm, st);
+    }
+    return err == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+KLA_API kla_status_t kla_gated_scan_step(const void *f, const void *x, kla_dtype_t in_dtype, kla_gate_t gate,
+                                         const float *h, float *h_out, int64_t B, int64_t H, int64_t N,
+                                         void *stream) {
+    if (B < 0 || H < 0 || N < 0 || !gate_ok(gate)) return KLA_ERR_INVALID_ARG;
+    if (!dtype_ok(in_dtype)) return KLA_ERR_UNSUPPORTED_DTYPE;
+    Sizes s;
+    if (!sizes(B, 1, H, N, gate, &s)) return KLA_ERR_INVALID_ARG;
+    if (s.n == 0) return KLA_OK;
+    if (!f || !x || !h || !h_out) return KLA_ERR_INVALID_ARG;
+    const int64_t e = dtype_size(in_dtype);
+    const Range outs[1] = {range_of(h_out, 4 * s.n)};
+    // in place (h_out == h) each thread reads its channels before it writes them
+    const Range ins[3] = {range_of(f, e * s.gates), range_of(x, e * s.n),
+                          range_of(h == h_out ? nullptr : h, 4 * s.n)};
+    if (any_overlap(outs, 1, ins, 3)) return KLA_ERR_INVALID_ARG;
+    GatedStepParams prm;
+    prm.f = f; prm.x = x; prm.h = h; prm.out = h_out; prm.C = s.n; prm.N = N;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool head = gate == KLA_GATE_HEAD;
+    const cudaError_t err =
+        in_dtype == KLA_F32 ? run_step<float>(prm, head, st) : run_step<__nv_bfloat16>(prm, head, st);
+    return err == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+KLA_API kla_status_t kla_gated_scan_backward_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N,
+                                                            kla_dtype_t in_dtype, kla_gate_t gate, size_t *bytes) {
+    if (!bytes || B < 0 || T < 0 || H < 0 || N < 0 || !gate_ok(gate)) return KLA_ERR_INVALID_ARG;
+    if (!dtype_ok(in_dtype)) return KLA_ERR_UNSUPPORTED_DTYPE;
+    Sizes s;
+    if (!sizes(B, T, H, N, gate, &s)) return KLA_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (gate == KLA_GATE_HEAD && s.n > 0) {
+        const int64_t parts = parts_of(N, 1);  // the narrowest tiles
+        if (parts > 1) *bytes = (size_t)(4 * parts * s.rows);
+    }
+    return KLA_OK;
+}
+
+KLA_API kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype, kla_gate_t gate, const float *h0,
+                                             const float *h, const float *g_h, void *grad_f, void *grad_x,
+                                             float *grad_h0, int64_t B, int64_t T, int64_t H, int64_t N,
+                                             void *workspace, size_t workspace_bytes, void *stream) {
+    size_t need = 0;
+    const kla_status_t ws = kla_gated_scan_backward_workspace_size(B, T, H, N, in_dtype, gate, &need);
+    if (ws != KLA_OK) return ws;
+    Sizes s;
+    sizes(B, T, H, N, gate, &s);
+    if (s.C == 0 || (!grad_f && !grad_x && !grad_h0)) return KLA_OK;
+    if (T > 0 && (!f || !g_h || (grad_f && !h))) return KLA_ERR_INVALID_ARG;
+    const int64_t e = dtype_size(in_dtype);
+    const Range outs[4] = {range_of(grad_f, e * s.gates), range_of(grad_x, e * s.n), range_of(grad_h0, 4 * s.C),
+                           range_of(workspace, (int64_t)workspace_bytes)};
+    const Range ins[4] = {range_of(f, e * s.gates), range_of(h0, 4 * s.C), range_of(h, 4 * s.n),
+                          range_of(g_h, 4 * s.n)};
+    if (any_overlap(outs, 4, ins, 4)) return KLA_ERR_INVALID_ARG;
+    if (grad_f && need) {
+        if (!workspace || workspace_bytes < need) return KLA_ERR_WORKSPACE_TOO_SMALL;
+        if (!aligned(workspace, 256)) return KLA_ERR_MISALIGNED;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {  // no token: the loss does not depend on the entering state
+        if (!grad_h0) return KLA_OK;
+        return cudaMemsetAsync(grad_h0, 0, (size_t)(4 * s.C), st) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    }
+
+    const bool head = gate == KLA_GATE_HEAD;
+    const void *p[5] = {head ? nullptr : f, g_h, grad_f ? h : nullptr, head ? nullptr : grad_f, grad_x};
+    const int64_t es[5] = {e, 4, 4, e, e};
+    const int vec = vec_of(in_dtype, s.HN, N, head, p, es, 5);
+    const Launch l = plan(B, T, H, N, head, vec, KLA_GATED_BACKWARD_L);
+    if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
+    const int64_t parts = head ? parts_of(N, vec) : 1;
+    GatedBackwardParams prm;
+    prm.g = l.g;
+    prm.f = f; prm.h0 = h0; prm.h = h; prm.gh = g_h;
+    prm.gf = grad_f; prm.gx = grad_x; prm.gh0 = grad_h0;
+    prm.partial = grad_f && parts > 1 ? static_cast<float *>(workspace) : nullptr;
+    prm.gates = s.rows;
+    prm.group = l.group;
+    cudaError_t err;
+    if (in_dtype == KLA_F32) {
+        if (vec == 1)
+            err = head ? run_backward<float, 1, true>(l, prm, st) : run_backward<float, 1, false>(l, prm, st);
+        else
+            err = head ? run_backward<float, KLA_GATED_VEC_F32, true>(l, prm, st)
+                       : run_backward<float, KLA_GATED_VEC_F32, false>(l, prm, st);
+    } else {
+        if (vec == 1)
+            err = head ? run_backward<__nv_bfloat16, 1, true>(l, prm, st)
+                       : run_backward<__nv_bfloat16, 1, false>(l, prm, st);
+        else
+            err = head ? run_backward<__nv_bfloat16, KLA_GATED_VEC_BF16, true>(l, prm, st)
+                       : run_backward<__nv_bfloat16, KLA_GATED_VEC_BF16, false>(l, prm, st);
+    }
+    if (err == cudaSuccess && prm.partial) {
+        const unsigned grid = (unsigned)std::min<int64_t>((s.rows + 255) / 256, (int64_t)sm_count() * 8);
+        if (in_dtype == KLA_F32)
+            kla_gated_reduce_kernel<float><<<grid, 256, 0, st>>>(prm.partial, static_cast<float *>(grad_f), s.rows,
+                                                                 (int)parts);
+        else
+            kla_gated_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
+                prm.partial, static_cast<__nv_bfloat16 *>(grad_f), s.rows, (int)parts);
+        err = cudaGetLastError();
+    }
+    return err == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}

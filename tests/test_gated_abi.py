@@ -1,0 +1,136 @@
+"""The gated recurrence without a GPU: argument checks that answer on the host, and
+the tests' reference gradients against differences."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from test_gated_gpu import reference, reference_backward
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from kalman_linear_attention_b200 import _build, api
+    _build.build()
+    return api.load_library()
+
+
+P = 1 << 20  # fake pointers, never dereferenced: every case returns before a launch
+
+
+def test_forward_and_step_argument_errors(lib):
+    fwd = lib.kla_gated_scan_forward
+    args = lambda **kw: [kw.get("f", P), kw.get("x", 2 * P), kw.get("dt", 0), kw.get("gate", 0), kw.get("h0", 3 * P),
+                         kw.get("h", 4 * P), kw.get("B", 1), kw.get("T", 8), kw.get("H", 2), kw.get("N", 4), None]
+    for bad in ("B", "T", "H", "N"):
+        assert fwd(*args(**{bad: -1})) == 1
+    assert fwd(*args(dt=2)) == 2
+    assert fwd(*args(gate=2)) == 1
+    assert fwd(*args(gate=-1)) == 1
+    for null in ("f", "x", "h"):
+        assert fwd(*args(**{null: None})) == 1
+    assert fwd(*args(h=P + 4)) == 1              # h overlaps f
+    assert fwd(*args(h=2 * P)) == 1              # h overlaps x
+    assert fwd(*args(h=3 * P)) == 1              # h overlaps h0
+    assert fwd(*args(B=1 << 40, T=1 << 40)) == 1  # sizes past int64
+    assert fwd(*args(B=1 << 31, T=1, H=64, N=1)) == 1  # more tiles than a grid holds
+    for empty in ("B", "T", "H", "N"):
+        assert fwd(*args(**{empty: 0}, f=None, x=None, h=None)) == 0
+    step = lib.kla_gated_scan_step
+    sargs = lambda **kw: [kw.get("f", P), kw.get("x", 2 * P), kw.get("dt", 0), kw.get("gate", 0), kw.get("h", 3 * P),
+                          kw.get("out", 4 * P), kw.get("B", 2), kw.get("H", 2), kw.get("N", 4), None]
+    assert step(*sargs(N=-1)) == 1
+    assert step(*sargs(dt=7)) == 2
+    assert step(*sargs(gate=5)) == 1
+    for null in ("f", "x", "h", "out"):
+        assert step(*sargs(**{null: None})) == 1
+    assert step(*sargs(out=3 * P + 4)) == 1      # neither in place nor apart
+    assert step(*sargs(out=2 * P)) == 1
+    assert step(*sargs(B=0)) == 0
+    assert step(*sargs(B=1 << 40, H=1 << 40)) == 1
+
+
+def test_backward_argument_errors(lib):
+    bwd = lib.kla_gated_scan_backward
+    names = ["f", "dt", "gate", "h0", "h", "g", "gf", "gx", "gh0", "B", "T", "H", "N", "ws", "wsb", "stream"]
+    base = dict(f=P, dt=0, gate=1, h0=2 * P, h=3 * P, g=4 * P, gf=5 * P, gx=6 * P, gh0=7 * P, B=1, T=8, H=2, N=64,
+                ws=8 * P, wsb=1 << 16, stream=None)
+    args = lambda **kw: [kw.get(n, base[n]) for n in names]
+    assert bwd(*args(T=-1)) == 1
+    assert bwd(*args(dt=3)) == 2
+    assert bwd(*args(gate=3)) == 1
+    for null in ("f", "g", "h"):
+        assert bwd(*args(**{null: None})) == 1
+    assert bwd(*args(gx=4 * P)) == 1             # a gradient over g_h
+    assert bwd(*args(gf=6 * P)) == 1             # two gradients on one another
+    assert bwd(*args(gh0=8 * P)) == 1            # over the workspace
+    assert bwd(*args(ws=None, wsb=0)) == 3
+    assert bwd(*args(wsb=8)) == 3
+    assert bwd(*args(ws=8 * P + 8)) == 6
+    assert bwd(*args(gf=None, gx=None, gh0=None)) == 0  # nothing wanted
+    assert bwd(*args(H=0, f=None)) == 0
+    out = ctypes.c_size_t(7)
+    size = lib.kla_gated_scan_backward_workspace_size
+    assert size(2, 100, 3, 64, 0, 1, ctypes.byref(out)) == 0 and out.value == 2 * 100 * 3 * 2 * 4
+    assert size(2, 100, 3, 32, 0, 1, ctypes.byref(out)) == 0 and out.value == 0
+    assert size(2, 100, 3, 64, 0, 0, ctypes.byref(out)) == 0 and out.value == 0
+    assert size(2, 0, 3, 64, 0, 1, ctypes.byref(out)) == 0 and out.value == 0
+    assert size(-1, 1, 1, 1, 0, 0, ctypes.byref(out)) == 1
+    assert size(1, 1, 1, 1, 9, 0, ctypes.byref(out)) == 2
+    assert size(1, 1, 1, 1, 0, 9, ctypes.byref(out)) == 1
+    assert size(1, 1, 1, 1, 0, 0, None) == 1
+    assert size(1 << 40, 1 << 40, 1, 1, 0, 0, ctypes.byref(out)) == 1
+
+
+def test_binding_refusals():
+    """Wrong shapes, types and places raise before the library is reached."""
+    import kalman_linear_attention_b200 as kla
+    f, x = torch.rand(2, 5, 3, 4), torch.rand(2, 5, 3, 4)
+    h0 = torch.zeros(2, 3, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        kla.gated_scan_forward(f, x, h0)
+    with pytest.raises(ValueError, match="f must be"):
+        kla.gated_scan_forward(f[:, :4], x)
+    with pytest.raises(ValueError, match="f must be"):
+        kla.gated_scan_forward(f[..., :1], x)
+    with pytest.raises(ValueError, match=r"\[B, T, H, N\]"):
+        kla.gated_scan_forward(f[0], x[0])
+    with pytest.raises(TypeError, match="share one dtype"):
+        kla.gated_scan_forward(f.bfloat16(), x)
+    with pytest.raises(TypeError):
+        kla.gated_scan_forward(f.half(), x.half())
+    with pytest.raises(ValueError, match="h0"):
+        kla.gated_scan_forward(f, x, h0[:1])
+    with pytest.raises(TypeError, match="h0"):
+        kla.gated_scan_forward(f, x, h0.double())
+    with pytest.raises(TypeError, match="out"):
+        kla.gated_scan_forward(f, x, out=torch.empty(2, 5, 3, 4, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match=r"\[B, H, N\]"):
+        kla.gated_scan_step(f, x, h0)
+    with pytest.raises(ValueError, match="h_state"):
+        kla.gated_scan_step(f[:, 0], x[:, 0], h0[:, :2])
+    with pytest.raises(TypeError, match="g_h"):
+        kla.gated_scan_backward(f, x, x.bfloat16())
+    with pytest.raises(ValueError, match="g_h"):
+        kla.gated_scan_backward(f, x, x[:, :3])
+
+
+def test_reference_gradient_against_differences():
+    """The reference's gradients are those of its forward pass: central
+    differences of a loss in fp64."""
+    rng = np.random.default_rng(0)
+    for gate_shape in ((2, 5, 2, 3), (2, 5, 2)):
+        f, x = rng.uniform(-1, 1, gate_shape), rng.standard_normal((2, 5, 2, 3))
+        g, h0 = rng.standard_normal(x.shape), rng.standard_normal((2, 2, 3))
+        h = reference(f, x, h0)[0]
+        want = reference_backward(f, h, g, h0, 0.0)
+        for name, a in (("f", f), ("x", x), ("h0", h0)):
+            for at in np.ndindex(*a.shape):
+                kept = a[at]
+                a[at] = kept + 1e-6
+                up = (reference(f, x, h0)[0] * g).sum()
+                a[at] = kept - 1e-6
+                down = (reference(f, x, h0)[0] * g).sum()
+                a[at] = kept
+                assert abs((up - down) / 2e-6 - want[name][0][at]) < 1e-7, (name, at)

@@ -1,0 +1,335 @@
+"""The gated linear recurrence (kla_gated_scan_*) against plain loops in fp64.
+
+Error bounds.  With u = 2^-24 and S_t = |f_t| S_{t-1} + |x_t| (S_-1 = |h0|, the
+recurrence on magnitudes), every token of the kernel's evaluation adds at most
+4 roundings relative to S_t, whatever spans it composes: one for the product
+of gates, one for the local state, one when a span's pair is applied and one
+when a cluster's are composed (the last two are shared by at least 16 tokens
+where the sequence has them).  An error once made decays with the gates, so
+
+    e_t <= |f_t| e_{t-1} + 4 u S_t
+
+bounds |h_t - exact|.  The backward scan obeys the same with g for x in
+reverse time; grad_f = E h adds |h| e and one rounding, a sum over a head's N
+channels one rounding for each addition on a term's way (two channels of a
+lane, 5 lane exchanges, the tiles of a head), and rounding to the inputs' type
+half a step of it (2^-24 or 2^-8) relative to the value.
+"""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+HALF_STEP = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+# B, T, H, N: one token, one warp, ragged chunks and tiles, several rounds,
+# clusters of 2 to 8 with a ragged end, heads that tiles do not divide
+SHAPES = [(1, 1, 1, 1), (2, 1, 3, 5), (1, 16, 1, 32), (2, 17, 3, 24), (1, 128, 2, 64), (2, 129, 2, 50),
+          (3, 300, 5, 7), (1, 1025, 1, 64), (2, 2500, 2, 128), (1, 4200, 4, 16), (40, 20, 8, 48),
+          (1, 333, 2, 200)]
+
+
+def _kla():
+    import kalman_linear_attention_b200 as kla
+    return kla
+
+
+def _inputs(shape, dtype, gate, with_h0, seed=0, gates="decay"):
+    B, T, H, N = shape
+    gen = torch.Generator().manual_seed(seed)
+    fshape = shape if gate == "channel" else shape[:3]
+    if gates == "decay":
+        f = torch.sigmoid(torch.randn(fshape, generator=gen, dtype=torch.float64) * 2 + 2)
+    else:  # any sign, a tenth of them 0
+        f = torch.rand(fshape, generator=gen, dtype=torch.float64) * 2.1 - 1.05
+        f[torch.rand(fshape, generator=gen) < 0.1] = 0
+    x = torch.randn(shape, generator=gen, dtype=torch.float64)
+    g = torch.randn(shape, generator=gen, dtype=torch.float64)
+    h0 = torch.randn((B, H, N), generator=gen, dtype=torch.float64) if with_h0 else None
+    f, x = f.to(dtype), x.to(dtype)
+    g, h0 = g.float(), None if h0 is None else h0.float()
+    return f, x, g, h0
+
+
+def _np(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def _full(f, shape):
+    return np.broadcast_to(f if f.ndim == len(shape) else f[..., None], shape)
+
+
+def reference(f, x, h0):
+    """States and their error bound, token after token in fp64."""
+    shape = x.shape
+    f = _full(f, shape)
+    B, T, H, N = shape
+    h = np.empty(shape)
+    e = np.empty(shape)
+    last = np.zeros((B, H, N)) if h0 is None else h0
+    mag, err = np.abs(last), np.zeros((B, H, N))
+    for t in range(T):
+        last = f[:, t] * last + x[:, t]
+        mag = np.abs(f[:, t]) * mag + np.abs(x[:, t])
+        err = np.abs(f[:, t]) * err + 4 * U * mag
+        h[:, t], e[:, t] = last, err
+    return h, e
+
+
+def reference_backward(f, h, g, h0, half_step):
+    """Gradients and their error bounds (for h as given)."""
+    head = f.ndim == 3
+    shape = h.shape
+    ff = _full(f, shape)
+    B, T, H, N = shape
+    later = np.concatenate([ff[:, 1:], np.zeros((B, 1, H, N))], 1)
+    E, eE = reference(later[:, ::-1], g[:, ::-1], None)
+    E, eE = E[:, ::-1], eE[:, ::-1]
+    first = np.zeros((B, 1, H, N)) if h0 is None else h0[:, None]
+    before = np.concatenate([first, h[:, :-1]], 1)
+    gf = E * before
+    egf = np.abs(before) * eE + U * np.abs(gf)
+    if head:
+        egf = egf.sum(-1) + (8 + N / 32) * U * np.abs(gf).sum(-1)
+        gf = gf.sum(-1)
+    gh0 = ff[:, 0] * E[:, 0]
+    return {"f": (gf, egf + half_step * (np.abs(gf) + egf)), "x": (E, eE + half_step * (np.abs(E) + eE)),
+            "h0": (gh0, np.abs(ff[:, 0]) * eE[:, 0] + U * np.abs(gh0))}
+
+
+def assert_within(got, ref, bound, what):
+    got = _np(got)
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} values off, the first at "
+                           f"{np.argwhere(bad)[0]}: {got[bad][0]} for {ref[bad][0]}, bound {bound[bad][0]:.3e}")
+
+
+def to_device(*ts):
+    return [None if t is None else t.to(DEV) for t in ts]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("gate", ["channel", "head"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_forward_and_backward(shape, gate, dtype):
+    kla = _kla()
+    for k, gates in enumerate(("decay", "any")):
+        f, x, g, h0 = _inputs(shape, dtype, gate, with_h0=k == 0, seed=k, gates=gates)
+        df, dx, dg, dh0 = to_device(f, x, g, h0)
+        h = kla.gated_scan_forward(df, dx, dh0)
+        assert h.dtype == torch.float32 and h.shape == dx.shape
+        ref, err = reference(_np(f), _np(x), _np(h0))
+        assert_within(h, ref, err, f"h, {gates} gates")
+        gf, gx, gh0 = kla.gated_scan_backward(df, h, dg, dh0)
+        assert gf.dtype == gx.dtype == dtype and gf.shape == df.shape
+        want = reference_backward(_np(f), _np(h), _np(g), _np(h0), HALF_STEP[dtype])
+        for name, got in zip(("f", "x", "h0"), (gf, gx, gh0)):
+            assert_within(got, *want[name], f"gradient of {name}, {gates} gates")
+
+
+@pytest.mark.parametrize("gate", ["channel", "head"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 3, 64), (1, 1, 1), (3, 5, 7), (4, 2, 6), (5, 3, 20)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_step_continues_the_scan(shape, gate, dtype):
+    """Token after token, in place and out of place: the states of the scan,
+    within one rounding of fp32 a token."""
+    kla = _kla()
+    B, H, N = shape
+    f, x, _, h0 = _inputs((B, 9, H, N), dtype, gate, True, seed=3)
+    ref, err = reference(_np(f), _np(x), _np(h0))
+    df, dx, dh0 = to_device(f, x, h0)
+    state, other = dh0.clone(), torch.empty_like(dh0)
+    for t in range(9):
+        kept = state.clone()
+        out = kla.gated_scan_step(df[:, t].contiguous(), dx[:, t].contiguous(), state, out=other)
+        assert out is other and torch.equal(state, kept)
+        assert kla.gated_scan_step(df[:, t].contiguous(), dx[:, t].contiguous(), state) is state
+        assert torch.equal(state, other)
+        assert_within(state, ref[:, t], err[:, t], f"state {t}")
+    h = kla.gated_scan_forward(df, dx, dh0)
+    assert_within(h[:, -1], ref[:, -1], err[:, -1], "last row of the scan")
+
+
+@pytest.mark.parametrize("gate", ["channel", "head"])
+def test_unaligned_arrays(gate):
+    """Arrays that start on any element (views into larger buffers) give the
+    values of aligned ones, within the bound."""
+    kla = _kla()
+    shape = (2, 70, 2, 34)
+    f, x, g, h0 = _inputs(shape, torch.bfloat16, gate, True, seed=5)
+
+    def shifted(t):
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
+        buf[1:] = t.to(DEV).reshape(-1)
+        return buf[1:].view(t.shape)
+
+    df, dx, dg, dh0 = (shifted(t) for t in (f, x, g, h0))
+    out = shifted(torch.zeros(shape))
+    h = kla.gated_scan_forward(df, dx, dh0, out=out)
+    assert h is out
+    ref, err = reference(_np(f), _np(x), _np(h0))
+    assert_within(h, ref, err, "h")
+    want = reference_backward(_np(f), _np(h), _np(g), _np(h0), HALF_STEP[torch.bfloat16])
+    for name, got in zip(("f", "x", "h0"), kla.gated_scan_backward(df, h, dg, dh0)):
+        assert_within(got, *want[name], f"gradient of {name}")
+    assert_within(kla.gated_scan_step(df[0, :2].contiguous(), dx[0, :2].contiguous(), shifted(dh0)),
+                  _full(_np(f)[0, :2], (2, 2, 34)) * _np(h0) + _np(x)[0, :2],
+                  2 * U * (np.abs(_full(_np(f)[0, :2], (2, 2, 34)) * _np(h0)) + np.abs(_np(x)[0, :2])), "step")
+
+
+@pytest.mark.parametrize("gate", ["channel", "head"])
+def test_values_that_are_not_finite_stay_in_their_channel(gate):
+    """An infinite or NaN input touches its own channel from its token on (for
+    a shared gate: the head's channels), in the gradients from it backwards."""
+    kla = _kla()
+    B, T, H, N = shape = (2, 300, 2, 40)
+    f, x, g, h0 = to_device(*_inputs(shape, torch.float32, gate, True, seed=7))
+    clean = kla.gated_scan_forward(f, x, h0)
+    for value in (float("inf"), float("nan")):
+        bad = x.clone()
+        bad[1, 150, 1, 7] = value
+        h = kla.gated_scan_forward(f, bad, h0)
+        same = torch.ones(shape, dtype=torch.bool, device=DEV)
+        same[1, 150:, 1, 7] = False
+        assert torch.equal(h[same], clean[same])
+        assert not torch.isfinite(h[1, 150, 1, 7])
+        badg = g.clone()
+        badg[0, 100, 0, 3] = value
+        gf, gx, gh0 = kla.gated_scan_backward(f, clean, g, h0)
+        bf, bx, bh0 = kla.gated_scan_backward(f, clean, badg, h0)
+        same[:] = True
+        same[0, :101, 0, 3] = False
+        assert torch.equal(bx[same], gx[same])
+        same_f = same if gate == "channel" else same.all(-1)
+        assert torch.equal(bf[same_f], gf[same_f])
+        assert not torch.isfinite(bh0[0, 0, 3])
+
+
+def test_a_gate_of_zero_starts_afresh():
+    """Sequences packed one after another: a zero gate at each start gives the
+    states of the sequences alone, from zero."""
+    kla = _kla()
+    lengths = [1, 40, 129, 3, 90]
+    f, x, _, _ = to_device(*_inputs((1, sum(lengths), 2, 40), torch.float32, "channel", False, seed=9))
+    at = 0
+    for n in lengths:
+        f[:, at] = 0
+        at += n
+    h = kla.gated_scan_forward(f, x)
+    at = 0
+    for n in lengths:
+        ref, err = reference(_np(f[:, at:at + n]), _np(x[:, at:at + n]), None)
+        assert_within(h[:, at:at + n], ref, err, f"sequence of {n}")
+        at += n
+
+
+@pytest.mark.parametrize("gate", ["channel", "head"])
+def test_autograd(gate):
+    """gated_scan: gradients of a loss on the states, of those wanted only, and
+    with a gradient that arrives transposed."""
+    kla = _kla()
+    f, x, g, h0 = to_device(*_inputs((2, 90, 3, 48), torch.float32, gate, True, seed=11))
+    leaves = [t.clone().requires_grad_() for t in (f, x, h0)]
+    h = kla.gated_scan(*leaves)
+    (h.transpose(1, 2) * g.transpose(1, 2)).sum().backward()
+    want = kla.gated_scan_backward(f, h.detach(), g, h0)
+    for leaf, w in zip(leaves, want):
+        assert torch.equal(leaf.grad, w)
+    only = x.clone().requires_grad_()
+    (kla.gated_scan(f, only) * g).sum().backward()
+    assert torch.equal(only.grad, want[1])  # dL/dx does not depend on h0
+    gated = f.clone().requires_grad_()
+    (kla.gated_scan(gated, x) * g).sum().backward()
+    assert gated.grad.shape == f.shape
+
+
+def test_empty_problems():
+    kla = _kla()
+    for shape in ((0, 5, 2, 3), (2, 0, 2, 3), (2, 5, 0, 3), (2, 5, 2, 0)):
+        f, x = torch.empty(shape, device=DEV), torch.empty(shape, device=DEV)
+        h0 = torch.full((shape[0], *shape[2:]), 2.0, device=DEV)
+        h = kla.gated_scan_forward(f, x, h0)
+        assert h.shape == shape
+        gf, gx, gh0 = kla.gated_scan_backward(f, h, torch.empty_like(h), h0)
+        assert gf.shape == gx.shape == shape and not gh0.any()
+    empty = torch.empty(0, 2, 3, device=DEV)
+    assert kla.gated_scan_step(empty, empty, empty).shape == (0, 2, 3)
+
+
+def test_same_bits_every_time_and_on_another_stream():
+    """The sums have a fixed order; a call on a stream that is not the current
+    one orders its own allocations there."""
+    kla = _kla()
+    f, x, g, h0 = to_device(*_inputs((1, 3000, 2, 96), torch.bfloat16, "head", True, seed=13))
+    torch.cuda.synchronize()
+    first = None
+    side = torch.cuda.Stream()
+    for k in range(4):
+        stream = side if k % 2 else None
+        h = kla.gated_scan_forward(f, x, h0, stream=stream)
+        got = (h, *kla.gated_scan_backward(f, h, g, h0, stream=stream))
+        torch.cuda.synchronize()
+        first = first or got
+        for a, b in zip(first, got):
+            assert torch.equal(a, b)
+
+
+def test_captured_and_replayed():
+    """Forward, backward and a step in one CUDA graph, replayed on new inputs
+    beside a second graph."""
+    kla = _kla()
+    shape = (2, 260, 2, 64)
+
+    def record(seed):
+        f, x, g, h0 = to_device(*_inputs(shape, torch.float32, "head", True, seed=seed))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            h = kla.gated_scan_forward(f, x, h0)
+            grads = kla.gated_scan_backward(f, h, g, h0)
+            nxt = kla.gated_scan_step(f[:, 0].contiguous(), x[:, 0].contiguous(), h[:, -1].contiguous())
+        return graph, (f, x, g, h0), (h, *grads, nxt)
+
+    graphs = [record(1), record(2)]
+    for seed in (3, 4):
+        for k, (graph, inputs, _) in enumerate(graphs):
+            for t, new in zip(inputs, _inputs(shape, torch.float32, "head", True, seed=seed + 10 * k)):
+                t.copy_(new)
+        for graph, _, _ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, (f, x, g, h0), got in graphs:
+            h = kla.gated_scan_forward(f, x, h0)
+            want = (h, *kla.gated_scan_backward(f, h, g, h0),
+                    kla.gated_scan_step(f[:, 0].contiguous(), x[:, 0].contiguous(), h[:, -1].contiguous()))
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last tokens follow from the states a few
+    tokens before them, and so do the first gradients."""
+    kla = _kla()
+    B, T, H, N = 2, 33000, 64, 512
+    assert B * T * H * N > 2 ** 31
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    f = torch.rand((B, T, H), generator=gen, device=DEV).to(torch.bfloat16)
+    x = torch.randn((B, T, H, N), generator=gen, device=DEV, dtype=torch.bfloat16)
+    h = kla.gated_scan_forward(f, x)
+    # the reference starts 400 tokens before the end from a state of unknown
+    # error, at most e times the product of the gates since: below 1e-30 of
+    # that state when the 200 compared tokens begin
+    k = 200
+    late = np.s_[-1:, -2 * k:, -1:]
+    ref, err = reference(_np(f[late]), _np(x[late]), _np(h[-1:, -2 * k - 1, -1:]))
+    assert np.prod(_np(f[-1:, -2 * k:-k, -1:])) < 1e-30
+    assert_within(h[-1:, -k:, -1:], ref[:, -k:], err[:, -k:], "last tokens")
+    del x
+    gf, gx, _ = kla.gated_scan_backward(f, h, h)  # the loss sum h^2 / 2
+    sl = np.s_[-1:, -k:, -1:]
+    want = reference_backward(_np(f[sl]), _np(h[sl]), _np(h[sl]), _np(h[-1:, -k - 1, -1:]),
+                              HALF_STEP[torch.bfloat16])
+    assert_within(gx[sl], *want["x"], "last gradients of x")
+    assert_within(gf[sl], *want["f"], "last gradients of f")
