@@ -581,6 +581,101 @@ kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype, kla_ga
                                      float *grad_h0, int64_t B, int64_t T, int64_t H, int64_t N,
                                      void *workspace, size_t workspace_bytes, void *stream);
 
+/* Longest row (elements of a head) of the kla_rotary_* and kla_qk_norm_rotary_* calls. */
+#define KLA_ROTARY_MAX_D 1024
+
+/*
+ * Rotary positions: for every row x (one head of one token) of D elements,
+ * the first rot_dim elements are turned pairwise by the token's position
+ * times the pair's frequency, and scaled; the others pass:
+ *
+ *   (y_i, y_j) = scale (x_i cos A - x_j sin A, x_i sin A + x_j cos A),
+ *   A = position inv_freq_p,   (i, j) = (p, p + rot_dim / 2), or the
+ *   neighbours (2p, 2p + 1) when `interleaved` is 1;  p < rot_dim / 2
+ *
+ *   x, x_strides   [B, T, H, D] input, dtype (read only); x_strides is a HOST
+ *                  array of the strides of B, T and H in elements (>= 0; the
+ *                  D elements of a row are neighbours), NULL = dense
+ *   inv_freq       [rot_dim / 2] fp64 frequencies, radians per position
+ *                  (NULL when rot_dim is 0).  Scaled schedules for long
+ *                  contexts are frequencies of their own, with `scale` the
+ *                  factor that they put on the rotated part (1 otherwise)
+ *   positions      int64 position of token t of batch row b at
+ *                  positions[b * position_stride + t] (position_stride 0: the
+ *                  same for every row); NULL: position0 + t.  Any integer of
+ *                  magnitude up to 2^53; angles are formed and reduced in
+ *                  fp64
+ *   inverse        1: the angles are negated (the transpose; with it, the
+ *                  gradient of x from the gradient of the output)
+ *   out            [B, T, H, D] dense, dtype (written, rounded once)
+ *
+ * 0 <= rot_dim <= D <= KLA_ROTARY_MAX_D, rot_dim even, any alignment; arrays
+ * and strides that allow 16-byte vectors are fastest.  An empty problem is
+ * valid.  out may not overlap the inputs.
+ */
+kla_status_t kla_rotary_forward(const void *x, const int64_t *x_strides, kla_dtype_t dtype,
+                                const double *inv_freq, int64_t rot_dim, int interleaved, float scale, int inverse,
+                                const int64_t *positions, int64_t position_stride, int64_t position0, void *out,
+                                int64_t B, int64_t T, int64_t H, int64_t D, void *stream);
+
+/*
+ * QK-Norm: the RMS norm of every head of queries and keys, and the rotation
+ * of the result as in kla_rotary_forward (none with rot_dim 0), in one pass:
+ *
+ *   y = R(position) (weight * x / sqrt(mean_D(x^2) + eps))
+ *
+ *   q, k             [B, T, Hq, D] and [B, T, Hk, D], dtype, each with strides
+ *                    as in kla_rotary_forward (slices of one packed
+ *                    projection, say); Hk may be 0 and k NULL then
+ *   q_weight, k_weight
+ *                    [D] fp32, or NULL for 1
+ *   eps              >= 0
+ *   q_out, k_out     dense, dtype (rounded once)
+ *
+ * The k and q of kla_layer_forward / kla_layer_step are such rows with D = Ns.
+ * Sums and statistics are fp32.
+ */
+kla_status_t kla_qk_norm_rotary_forward(const void *q, const int64_t *q_strides, const void *k,
+                                        const int64_t *k_strides, kla_dtype_t dtype, const float *q_weight,
+                                        const float *k_weight, float eps, const double *inv_freq, int64_t rot_dim,
+                                        int interleaved, float scale, const int64_t *positions,
+                                        int64_t position_stride, int64_t position0, void *q_out, void *k_out,
+                                        int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D, void *stream);
+
+/*
+ * Device workspace that kla_qk_norm_rotary_backward needs when a weight's
+ * gradient is wanted (one row of sums per CTA), written to *bytes.
+ */
+kla_status_t kla_qk_norm_rotary_backward_workspace_size(int64_t Hq, int64_t Hk, int64_t D, size_t *bytes);
+
+/*
+ * Gradients of a scalar loss through kla_qk_norm_rotary_forward.  With r = 1 /
+ * sqrt(mean(x^2) + eps) formed again from x, g' = R(position)^T g and u =
+ * weight g':
+ *
+ *   d/d x = r (u - x r^2 mean(u x)),   d/d weight = sum over rows of g' x r
+ *
+ *   g_q, g_k         dense gradients of q_out and k_out, dtype
+ *   grad_q, grad_k   dense, dtype (rounded once), or NULL
+ *   grad_q_weight, grad_k_weight
+ *                    [D] fp32, or NULL; the sums over rows have a fixed order
+ *   workspace        at least kla_qk_norm_rotary_backward_workspace_size(...)
+ *                    bytes, 256-byte aligned, when a weight's gradient is
+ *                    wanted (else NULL); contents on entry do not matter.
+ *                    Concurrent calls need their own.
+ *
+ * The other arguments as in the forward call.  Without rows the weights'
+ * gradients are zero.  Outputs must not overlap inputs, the workspace or each
+ * other.
+ */
+kla_status_t kla_qk_norm_rotary_backward(
+    const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, kla_dtype_t dtype,
+    const float *q_weight, const float *k_weight, float eps, const double *inv_freq, int64_t rot_dim,
+    int interleaved, float scale, const int64_t *positions, int64_t position_stride, int64_t position0,
+    const void *g_q, const void *g_k, void *grad_q, void *grad_k, float *grad_q_weight, float *grad_k_weight,
+    int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D, void *workspace, size_t workspace_bytes,
+    void *stream);
+
 /*
  * Synchronise `stream`, then report the first failure since the previous
  * call on the current device: KLA_ERR_CUDA for a CUDA error (sticky or not),

@@ -16,6 +16,8 @@ _API_NAMES = {
     "attention_weights", "scan_forward_lti", "lti_workspace_size", "lti_plan",
     "gated_scan_forward", "gated_scan_step", "gated_scan_backward", "gated_scan_backward_workspace_size",
     "GatedScan", "gated_scan",
+    "rotary_frequencies", "rotary_forward", "Rotary", "rotary", "qk_norm_rotary_forward", "qk_norm_rotary_backward",
+    "qk_norm_rotary_backward_workspace_size", "QKNormRotary", "qk_norm_rotary", "QKNorm",
 }
 
 

@@ -8,8 +8,9 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
-from typing import Optional, Sequence, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -80,8 +81,19 @@ SIGNATURES = {
                                                               ctypes.POINTER(_SZ)]),
     "kla_gated_scan_backward": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.c_int, _VP, _VP, _VP, _VP, _VP, _VP, _I64,
                                                _I64, _I64, _I64, _VP, _SZ, _VP]),
+    "kla_rotary_forward": (ctypes.c_int, [_VP, _VP, ctypes.c_int, _VP, _I64, ctypes.c_int, ctypes.c_float,
+                                          ctypes.c_int, _VP, _I64, _I64, _VP, _I64, _I64, _I64, _I64, _VP]),
+    "kla_qk_norm_rotary_forward": (ctypes.c_int, [_VP, _VP, _VP, _VP, ctypes.c_int, _VP, _VP, ctypes.c_float, _VP,
+                                                  _I64, ctypes.c_int, ctypes.c_float, _VP, _I64, _I64, _VP, _VP,
+                                                  _I64, _I64, _I64, _I64, _I64, _VP]),
+    "kla_qk_norm_rotary_backward_workspace_size": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
+    "kla_qk_norm_rotary_backward": (ctypes.c_int, [_VP, _VP, _VP, _VP, ctypes.c_int, _VP, _VP, ctypes.c_float, _VP,
+                                                   _I64, ctypes.c_int, ctypes.c_float, _VP, _I64, _I64, _VP, _VP,
+                                                   _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _VP, _SZ,
+                                                   _VP]),
 }
 ATTENTION_MAX_WINDOW = 64  # KLA_ATTENTION_MAX_WINDOW
+ROTARY_MAX_D = 1024  # KLA_ROTARY_MAX_D
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -446,6 +458,25 @@ def kalman_filter(a: torch.Tensor, p: torch.Tensor, phi: torch.Tensor, b: torch.
 
 
 # ------------------------------------------------------------ fused layer
+class QKNorm(NamedTuple):
+    """What layer_forward and layer_step do to k and q first
+    (qk_norm_rotary_forward with D = Ns): weights [Ns] fp32 or None, and the
+    rotation (none without inv_freq)."""
+    q_weight: Optional[torch.Tensor] = None
+    k_weight: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+    inv_freq: Optional[torch.Tensor] = None
+    interleaved: bool = False
+    scale: float = 1.0
+
+
+def _normed(norm: QKNorm, k, q, positions, position0, stream):
+    q, k = qk_norm_rotary_forward(q, k, norm.q_weight, norm.k_weight, norm.inv_freq, positions,
+                                  position0=position0, eps=norm.eps, interleaved=norm.interleaved,
+                                  scale=norm.scale, stream=stream)
+    return k, q
+
+
 def layer_workspace_size(B: int, T: int, H: int, D: int, Ns: int, dtype: torch.dtype = torch.float32) -> int:
     code = KLA_BF16 if dtype == torch.bfloat16 else KLA_F32
     out = ctypes.c_size_t(0)
@@ -457,6 +488,7 @@ def layer_workspace_size(B: int, T: int, H: int, D: int, Ns: int, dtype: torch.d
 def layer_forward(k: torch.Tensor, q: torch.Tensor, v: torch.Tensor, w: torch.Tensor,
                   a: torch.Tensor, p: torch.Tensor, lam0: torch.Tensor, eta0: torch.Tensor, *,
                   want_s: bool = True, want_state: bool = True,
+                  qk_norm: Optional[QKNorm] = None, positions: Optional[torch.Tensor] = None, position0: int = 0,
                   out: Optional[Sequence[Optional[torch.Tensor]]] = None,
                   workspace: Optional[torch.Tensor] = None,
                   stream: Optional[torch.cuda.Stream] = None):
@@ -464,7 +496,9 @@ def layer_forward(k: torch.Tensor, q: torch.Tensor, v: torch.Tensor, w: torch.Te
     (kla_layer_forward): k, q [B, T, H, Ns]; v, w [B, T, H, D] (one dtype,
     fp32 or bf16); a, p [H, D, Ns] fp32; lam0, eta0 [B, H, D, Ns] fp32.
     Returns (y, s, lam_T, eta_T): y, s fp32 [B, T, H, D], the final state fp32
-    [B, H, D, Ns]; s / the state are None when not wanted."""
+    [B, H, D, Ns]; s / the state are None when not wanted.  With ``qk_norm``, k
+    and q are normalised (and rotated by ``positions``, or position0 + t) first
+    and may be strided."""
     if k.dim() != 4 or q.shape != k.shape or v.dim() != 4 or w.shape != v.shape:
         raise ValueError("k, q must be [B, T, H, Ns] and v, w [B, T, H, D]")
     if not (k.dtype == q.dtype == v.dtype == w.dtype):
@@ -478,6 +512,10 @@ def layer_forward(k: torch.Tensor, q: torch.Tensor, v: torch.Tensor, w: torch.Te
     for t in (a, p, lam0, eta0):
         if t.dtype != torch.float32:
             raise TypeError("a, p, lam0, eta0 must be float32")
+    if qk_norm is not None:
+        k, q = _normed(qk_norm, k, q, positions, position0, stream)
+    elif positions is not None or position0:
+        raise ValueError("positions need qk_norm")
     _require_cuda(k, q, v, w, a, p, lam0, eta0)
     dev = k.device
     if out is None:
@@ -503,10 +541,13 @@ def layer_forward(k: torch.Tensor, q: torch.Tensor, v: torch.Tensor, w: torch.Te
 def layer_step(k: torch.Tensor, q: torch.Tensor, v: torch.Tensor, w: torch.Tensor,
                a: torch.Tensor, p: torch.Tensor, lam_state: torch.Tensor, eta_state: torch.Tensor, *,
                y: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None, want_s: bool = True,
+               qk_norm: Optional[QKNorm] = None, positions: Optional[torch.Tensor] = None, position0: int = 0,
                stream: Optional[torch.cuda.Stream] = None):
     """One decode token of the fused layer (kla_layer_step): k, q [B, H, Ns];
     v, w [B, H, D]; a, p [H, D, Ns]; the state [B, H, D, Ns] is updated in
-    place.  Returns (y, s), fp32 [B, H, D] (s None when not wanted)."""
+    place.  Returns (y, s), fp32 [B, H, D] (s None when not wanted).  With
+    ``qk_norm``, k and q are normalised (and rotated by the positions [B], or
+    position0) first."""
     if k.dim() != 3 or q.shape != k.shape or v.dim() != 3 or w.shape != v.shape:
         raise ValueError("k, q must be [B, H, Ns] and v, w [B, H, D]")
     if not (k.dtype == q.dtype == v.dtype == w.dtype):
@@ -515,6 +556,11 @@ def layer_step(k: torch.Tensor, q: torch.Tensor, v: torch.Tensor, w: torch.Tenso
     D = v.shape[2]
     if tuple(v.shape[:2]) != (B, H) or lam_state.shape != (B, H, D, Ns) or eta_state.shape != (B, H, D, Ns):
         raise ValueError("v, w must be [B, H, D] and the state [B, H, D, Ns]")
+    if qk_norm is not None:
+        at = None if positions is None else positions.unsqueeze(-1)
+        k, q = (t.squeeze(1) for t in _normed(qk_norm, k.unsqueeze(1), q.unsqueeze(1), at, position0, stream))
+    elif positions is not None or position0:
+        raise ValueError("positions need qk_norm")
     _require_cuda(k, q, v, w, a, p, lam_state, eta_state, y, s)
     if y is None:
         y = torch.empty((B, H, D), dtype=torch.float32, device=k.device)
@@ -785,3 +831,252 @@ def gated_scan(f: torch.Tensor, x: torch.Tensor, h0: Optional[torch.Tensor] = No
     """The states of the gated recurrence, differentiable with respect to
     f, x and h0 through the CUDA backward scan."""
     return GatedScan.apply(f, x, h0)
+
+
+# ---------------------------------------- QK norm and rotary positions
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                       length: int = 4096, fast: float = 32.0, slow: float = 1.0,
+                       device=None) -> Tuple[torch.Tensor, float]:
+    """(inv_freq, scale) for rotary and qk_norm_rotary: inv_freq [rot_dim / 2]
+    fp64, base^(-2 i / rot_dim) radians per position, made for contexts
+    ``factor`` times as long as the ``length`` a model was trained on:
+
+    * ``"none"``: as it is;
+    * ``"linear"``: every position divided by ``factor``;
+    * ``"ntk"``: the base raised, so that the slowest pair turns ``factor``
+      times slower and the fastest keeps its angle;
+    * ``"yarn"``: pairs that make more than ``fast`` turns over ``length`` keep
+      their angle, those with fewer than ``slow`` are divided by ``factor``,
+      with a linear ramp over the turns between; scale = 0.1 ln(factor) + 1.
+    """
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and not negative")
+    if not factor >= 1.0:
+        raise ValueError("factor must be at least 1")
+    if not base > 0.0:
+        raise ValueError("base must be positive")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "ntk" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    inv_freq = base ** (-i / max(rot_dim, 1))
+    if scaling == "linear":
+        inv_freq = inv_freq / factor
+    elif scaling == "yarn":
+        if not fast > slow:
+            raise ValueError("fast must be above slow")
+        keep = ((length * inv_freq / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        inv_freq = inv_freq / factor * (1 - keep) + inv_freq * keep
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"scaling must be none, linear, ntk or yarn, got {scaling!r}")
+    return inv_freq.to(device) if device is not None else inv_freq, scale
+
+
+def _head_rows(name: str, t: torch.Tensor, like: torch.Tensor):
+    """The host array of the strides of [B, T, H, D] rows (None: dense)."""
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, as the other tensors are")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        return None
+    sb, st, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return (ctypes.c_int64 * 3)(sb, st, sh)
+
+
+def _rotation(like: torch.Tensor, B: int, T: int, D: int, inv_freq: Optional[torch.Tensor],
+              positions: Optional[torch.Tensor]):
+    """(inv_freq pointer, rot_dim, positions pointer, batch stride)."""
+    dev = like.device
+    if inv_freq is None:
+        if positions is not None:
+            raise ValueError("positions need inv_freq")
+        return None, 0, None, 0
+    if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > D:
+        raise ValueError(f"inv_freq must be [rot_dim / 2] with rot_dim at most {D}, got {list(inv_freq.shape)}")
+    if inv_freq.dtype != torch.float64:
+        raise TypeError(f"inv_freq must be torch.float64, got {inv_freq.dtype}")
+    _require_like(dev, inv_freq=inv_freq)
+    if positions is None:
+        return inv_freq.data_ptr(), 2 * inv_freq.shape[0], None, 0
+    if positions.dtype != torch.int64:
+        raise TypeError(f"positions must be torch.int64, got {positions.dtype}")
+    if positions.device != dev:
+        raise ValueError(f"positions must be on {dev}, as the other tensors are")
+    if positions.shape == (T,):
+        batch = 0
+    elif positions.shape == (B, T):
+        batch = positions.stride(0) if B > 1 else 0
+    else:
+        raise ValueError(f"positions must be [{B}, {T}] or [{T}], got {list(positions.shape)}")
+    if T > 1 and positions.stride(-1) != 1:
+        raise ValueError("the last axis of positions must be contiguous")
+    return inv_freq.data_ptr(), 2 * inv_freq.shape[0], positions.data_ptr(), batch
+
+
+def rotary_forward(x: torch.Tensor, inv_freq: torch.Tensor, positions: Optional[torch.Tensor] = None, *,
+                   position0: int = 0, interleaved: bool = False, scale: float = 1.0, inverse: bool = False,
+                   out: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Rotary positions (kla_rotary_forward): the first 2 len(inv_freq)
+    elements of every row of x [B, T, H, D] (fp32 or bf16; any strides of B, T,
+    H) turned by position times frequency.  inv_freq fp64
+    (rotary_frequencies); positions int64 [B, T] or [T], or None for position0
+    + t; ``interleaved``: neighbours form a pair, else the two halves do;
+    ``inverse``: the other way round.  Returns a dense tensor of x's type."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B, T, H, D]")
+    B, T, H, D = x.shape
+    code = _dtype_code(x)
+    strides = _head_rows("x", x, x)
+    freq, rot, pos, batch = _rotation(x, B, T, D, inv_freq, positions)
+    _require_shape("out", out, x.shape, x.dtype)
+    _require_like(x.device, out=out)
+    with _Launch(x, stream) as on:
+        if out is None:
+            out = on.empty(x.shape, x.dtype)
+        st = lib().kla_rotary_forward(_ptr(x), strides, code, freq, rot, int(interleaved), scale, int(inverse), pos,
+                                      batch, position0, _ptr(out), B, T, H, D, on.handle)
+    _check(st, "kla_rotary_forward")
+    return out
+
+
+class Rotary(torch.autograd.Function):
+    """Differentiable rotary_forward: the gradient is the inverse rotation."""
+
+    @staticmethod
+    def forward(ctx, x, inv_freq, positions, position0, interleaved, scale):
+        ctx.rotation = dict(position0=position0, interleaved=interleaved, scale=scale)
+        ctx.save_for_backward(inv_freq, positions)
+        return rotary_forward(x, inv_freq, positions, **ctx.rotation)
+
+    @staticmethod
+    def backward(ctx, g):
+        inv_freq, positions = ctx.saved_tensors
+        return (rotary_forward(g.contiguous(), inv_freq, positions, inverse=True, **ctx.rotation),
+                None, None, None, None, None)
+
+
+def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions: Optional[torch.Tensor] = None, *,
+           position0: int = 0, interleaved: bool = False, scale: float = 1.0) -> torch.Tensor:
+    """rotary_forward, differentiable with respect to x."""
+    return Rotary.apply(x, inv_freq, positions, position0, interleaved, scale)
+
+
+def _qk_shapes(q: torch.Tensor, k: torch.Tensor) -> Tuple[int, int, int, int, int]:
+    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+        raise ValueError("q must be [B, T, Hq, D] and k [B, T, Hk, D]")
+    B, T, Hq, D = q.shape
+    return B, T, Hq, k.shape[2], D
+
+
+def qk_norm_rotary_forward(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                           k_weight: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
+                           positions: Optional[torch.Tensor] = None, *, position0: int = 0, eps: float = 1e-6,
+                           interleaved: bool = False, scale: float = 1.0,
+                           out: Optional[Sequence[torch.Tensor]] = None,
+                           stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """QK-Norm with the position rotation in the same pass
+    (kla_qk_norm_rotary_forward): q [B, T, Hq, D], k [B, T, Hk, D] (one of fp32
+    and bf16; any strides of B, T, H, so slices of a packed projection); the
+    RMS norm of each head, times the weight ([D] fp32 or None), rotated as in
+    rotary_forward (not at all without inv_freq).  Returns dense (q, k) of the
+    inputs' type."""
+    B, T, Hq, Hk, D = _qk_shapes(q, k)
+    code = _dtype_code(q)
+    qs, ks = _head_rows("q", q, q), _head_rows("k", k, q)
+    freq, rot, pos, batch = _rotation(q, B, T, D, inv_freq, positions)
+    _require_shape("q_weight", q_weight, (D,), torch.float32)
+    _require_shape("k_weight", k_weight, (D,), torch.float32)
+    _require_like(q.device, q_weight=q_weight, k_weight=k_weight)
+    q_out, k_out = (None, None) if out is None else out
+    _require_shape("out", q_out, q.shape, q.dtype)
+    _require_shape("out", k_out, k.shape, q.dtype)
+    _require_like(q.device, q_out=q_out, k_out=k_out)
+    with _Launch(q, stream) as on:
+        if out is None:
+            q_out, k_out = on.empty(q.shape, q.dtype), on.empty(k.shape, q.dtype)
+        st = lib().kla_qk_norm_rotary_forward(
+            _ptr(q), qs, _ptr(k), ks, code, _ptr(q_weight), _ptr(k_weight), eps, freq, rot, int(interleaved), scale,
+            pos, batch, position0, _ptr(q_out), _ptr(k_out), B, T, Hq, Hk, D, on.handle)
+    _check(st, "kla_qk_norm_rotary_forward")
+    return q_out, k_out
+
+
+def qk_norm_rotary_backward_workspace_size(Hq: int, Hk: int, D: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().kla_qk_norm_rotary_backward_workspace_size(Hq, Hk, D, ctypes.byref(out)),
+           "kla_qk_norm_rotary_backward_workspace_size")
+    return int(out.value)
+
+
+def qk_norm_rotary_backward(q: torch.Tensor, k: torch.Tensor, g_q: Optional[torch.Tensor],
+                            g_k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                            k_weight: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
+                            positions: Optional[torch.Tensor] = None, *, position0: int = 0, eps: float = 1e-6,
+                            interleaved: bool = False, scale: float = 1.0, want: Sequence[bool] = (True,) * 4,
+                            workspace: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> Tuple[Optional[torch.Tensor], ...]:
+    """Gradients through qk_norm_rotary_forward (kla_qk_norm_rotary_backward):
+    its inputs and the gradients g_q, g_k of its outputs (dense, the inputs'
+    type; None = zero).  Returns the gradients with respect to (q, k, q_weight,
+    k_weight): the first two dense in the inputs' type, the weights' fp32;
+    None where ``want`` is False, where there is no weight, or where the
+    output's gradient is None."""
+    B, T, Hq, Hk, D = _qk_shapes(q, k)
+    code = _dtype_code(q)
+    qs, ks = _head_rows("q", q, q), _head_rows("k", k, q)
+    freq, rot, pos, batch = _rotation(q, B, T, D, inv_freq, positions)
+    _require_shape("q_weight", q_weight, (D,), torch.float32)
+    _require_shape("k_weight", k_weight, (D,), torch.float32)
+    _require_shape("g_q", g_q, q.shape, q.dtype)
+    _require_shape("g_k", g_k, k.shape, q.dtype)
+    _require_like(q.device, q_weight=q_weight, k_weight=k_weight, g_q=g_q, g_k=g_k, workspace=workspace)
+    want = (want[0] and g_q is not None, want[1] and g_k is not None,
+            want[2] and g_q is not None and q_weight is not None,
+            want[3] and g_k is not None and k_weight is not None)
+    with _Launch(q, stream) as on:
+        gq = on.empty(q.shape, q.dtype) if want[0] else None
+        gk = on.empty(k.shape, q.dtype) if want[1] else None
+        gqw = on.empty((D,), torch.float32) if want[2] else None
+        gkw = on.empty((D,), torch.float32) if want[3] else None
+        if workspace is None and (want[2] or want[3]):
+            n = qk_norm_rotary_backward_workspace_size(Hq, Hk, D)
+            workspace = on.empty(n, torch.uint8) if n else None
+        st = lib().kla_qk_norm_rotary_backward(
+            _ptr(q), qs, _ptr(k), ks, code, _ptr(q_weight), _ptr(k_weight), eps, freq, rot, int(interleaved), scale,
+            pos, batch, position0, _ptr(g_q), _ptr(g_k), _ptr(gq), _ptr(gk), _ptr(gqw), _ptr(gkw), B, T, Hq, Hk, D,
+            _ptr(workspace), workspace.numel() if workspace is not None else 0, on.handle)
+    _check(st, "kla_qk_norm_rotary_backward")
+    return gq, gk, gqw, gkw
+
+
+class QKNormRotary(torch.autograd.Function):
+    """Differentiable QK-Norm with rotation: forward =
+    kla_qk_norm_rotary_forward, backward = kla_qk_norm_rotary_backward."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, inv_freq, positions, position0, eps, interleaved, scale):
+        ctx.set_materialize_grads(False)
+        ctx.options = dict(position0=position0, eps=eps, interleaved=interleaved, scale=scale)
+        ctx.save_for_backward(q, k, q_weight, k_weight, inv_freq, positions)
+        return qk_norm_rotary_forward(q, k, q_weight, k_weight, inv_freq, positions, **ctx.options)
+
+    @staticmethod
+    def backward(ctx, g_q, g_k):
+        q, k, *rest = ctx.saved_tensors
+        grads = [None if g is None else g.contiguous() for g in (g_q, g_k)]
+        got = qk_norm_rotary_backward(q, k, *grads, *rest, **ctx.options, want=ctx.needs_input_grad[:4])
+        return (*got, None, None, None, None, None, None)
+
+
+def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                   k_weight: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
+                   positions: Optional[torch.Tensor] = None, *, position0: int = 0, eps: float = 1e-6,
+                   interleaved: bool = False, scale: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
+    """qk_norm_rotary_forward, differentiable with respect to q, k and the
+    weights."""
+    return QKNormRotary.apply(q, k, q_weight, k_weight, inv_freq, positions, position0, eps, interleaved, scale)
