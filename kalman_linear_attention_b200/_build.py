@@ -16,7 +16,7 @@ DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path
 NVCC_FLAGS = [
     "-O3", "-std=c++17",
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-lineinfo",
+    "-lineinfo", "--threads", "0",
     "-Xcompiler", "-fPIC,-fvisibility=hidden",
     "-shared",
 ]

@@ -12,6 +12,11 @@ namespace {
 
 using namespace kla_mixer;
 
+// (Overridable at build time for tuning sweeps.)
+#ifndef KLA_ROTARY_ROWS
+#define KLA_ROTARY_ROWS 8
+#endif
+
 // What one call works on, checked: everything but the tensors.
 struct Call {
     RotaryParams prm = {};
@@ -75,13 +80,15 @@ bool set_input(const Call &c, const void *x, const int64_t *strides, int64_t hea
     return true;
 }
 
-// The widest vector (16 bytes at most) that divides the halves of the rotated
-// part, the rest of a row and the strides, and on which the arrays start.
+// The widest vector (16 bytes at most) on which the arrays start and that
+// divides the strides and a row, and with pairs of halves also the halves and
+// the rest of the row.
 void choose_vec(Call *c, int tensors) {
     const int64_t e = dtype_size(c->dtype);
-    int vec = (int)(16 / e);
+    const int64_t rest = c->D - 2 * c->prm.half;
+    const bool halves = c->prm.half > 0 && !c->prm.interleaved;
     auto fits = [&](int v) {
-        if (c->prm.half % v != 0 || (c->D - 2 * c->prm.half) % v != 0) return false;
+        if (c->D % v != 0 || (halves && (c->prm.half % v != 0 || rest % v != 0))) return false;
         for (int i = 0; i < tensors; ++i) {
             const RotaryTensor &t = c->prm.t[i];
             if (t.sb % v != 0 || t.st % v != 0 || t.sh % v != 0) return false;
@@ -90,71 +97,113 @@ void choose_vec(Call *c, int tensors) {
         }
         return true;
     };
-    while (vec > 1 && !fits(vec)) vec /= 2;
-    c->vec = vec;
-    const int64_t rest = c->D - 2 * c->prm.half;
-    c->prm.units = (int)(c->prm.half / vec + (rest + 2 * vec - 1) / (2 * vec));
+    c->vec = (int)(16 / e);
+    while (c->vec > 1 && !fits(c->vec)) c->vec /= 2;
+    c->prm.units = (int)((c->D + 2 * c->vec - 1) / (2 * c->vec));
+    // narrow vectors: four units a lane, so that a row is not spread over more
+    // lanes than its size is worth
+    const int least = c->vec > 2 ? 1 : 4;
     int lanes = 1;
-    while (lanes < 32 && lanes < c->prm.units) lanes *= 2;
+    while (lanes < 32 && lanes * least < c->prm.units) lanes *= 2;
     c->prm.lanes = lanes;
     c->upl = (c->prm.units + lanes - 1) / lanes;
 }
 
-// Rows that a group of lanes takes from a block of tokens, when there are
-// enough of them.
-constexpr int kRowsPerGroup = 4;
-
-// Blocks of tokens for each tensor; `cap` bounds the CTAs (0: one a block).
-void choose_blocks(Call *c, int tensors, int64_t cap) {
-    const int groups = kRotaryThreads / c->prm.lanes;
-    int64_t rows = 0;
-    for (int i = 0; i < tensors; ++i) rows += (int64_t)c->prm.t[i].heads;
+// How warps share a tensor's tokens and heads.  A group takes KLA_ROTARY_ROWS
+// heads of a token where there are tokens enough to fill the SMs with warps,
+// fewer where there are not.  At most as many CTAs as are resident at once; the tensors share them by their rows and what an item costs beyond
+// its rows (about two rows' time: cos and sin, the first copies).
+void choose_items(Call *c, int tensors, bool backward) {
+    const int64_t cap = (int64_t)sm_count() * rotary_resident(c->vec, c->upl, backward);
+    const int64_t warps = kRotaryThreads / 32, abreast = 32 / c->prm.lanes;
+    const int64_t fill = cap * warps;
+    int64_t work[2] = {0, 0}, need[2] = {0, 0};
     for (int i = 0; i < tensors; ++i) {
         RotaryTensor &t = c->prm.t[i];
-        const int64_t h = std::max(1, t.heads);
-        int64_t n = std::max<int64_t>(1, (int64_t)kRowsPerGroup * groups / h);
-        // small problems: spread over the SMs first
-        n = std::min(n, std::max<int64_t>(1, c->prm.tokens / (2 * sm_count())));
-        if (c->prm.half > 0) n = std::min<int64_t>(n, std::max(1, kRotaryTable / c->prm.half));
-        t.tokens_per_cta = (int)n;
-        int64_t ctas = t.heads > 0 ? (c->prm.tokens + n - 1) / n : 0;
-        if (cap > 0) ctas = std::min(ctas, std::max<int64_t>(1, cap * t.heads / std::max<int64_t>(1, rows)));
-        t.ctas = (unsigned)std::min<int64_t>(ctas, kMaxGrid / 2);
+        const int64_t h = t.heads;
+        if (h == 0 || c->prm.tokens == 0) continue;
+        // heads that a warp takes at once: few, so that a group has many heads
+        // and cos and sin serve them all; more where warps would be idle
+        int64_t n = 1;
+        while (n < abreast && n < h && (n * KLA_ROTARY_ROWS < h || c->prm.tokens * n < fill * abreast)) n *= 2;
+        t.abreast = (int)n;
+        const int64_t shares = (c->prm.tokens + abreast / n - 1) / (abreast / n);
+        const int64_t most = (h + n - 1) / n;  // one head a group
+        int64_t splits = (most + KLA_ROTARY_ROWS - 1) / KLA_ROTARY_ROWS;
+        splits = std::max(splits, std::min(most, fill / std::max<int64_t>(1, shares)));
+        t.splits = (int)splits;
+        const int64_t items = shares > kMaxGrid ? kMaxGrid : shares * splits;  // enough to fill any grid
+        need[i] = (items + warps - 1) / warps;
+        work[i] = items * ((most + splits - 1) / splits + 2);
     }
+    const double all = (double)work[0] + (double)work[1];
+    for (int i = 0; i < tensors; ++i)
+        if (need[i] > 0)
+            c->prm.t[i].ctas = (unsigned)(need[0] + need[1] <= cap
+                                              ? need[i]
+                                              : std::min(need[i], std::max<int64_t>(1, (int64_t)(cap * (work[i] / all)))));
+}
+
+// Pairs of cos and sin that a warp makes at once: those of its tokens.
+int table_pairs(const Call &c) {
+    int most = 0;
+    for (const RotaryTensor &t : c.prm.t)
+        if (t.ctas > 0) most = std::max(most, 32 / c.prm.lanes / t.abreast * c.prm.half);
+    return most;
 }
 
 template <typename T, int VEC, int UPL, bool NORM, bool BACKWARD>
 cudaError_t launch(const Call &c, cudaStream_t st) {
     const unsigned grid = c.prm.t[0].ctas + c.prm.t[1].ctas;
     if (grid == 0) return cudaSuccess;
-    size_t smem = 0;
-    for (const RotaryTensor &t : c.prm.t)
-        smem = std::max(smem, (size_t)t.tokens_per_cta * c.prm.half * sizeof(float2));
-    if (BACKWARD) smem = std::max(smem, (size_t)(kRotaryThreads / 32) * c.prm.D * sizeof(float));  // <= 32 KB
-    kla_rotary_kernel<T, VEC, UPL, NORM, BACKWARD><<<grid, kRotaryThreads, smem, st>>>(c.prm);
+    const int pairs = table_pairs(c);
+    size_t smem = (kRotaryThreads / 32) * (size_t)RotaryShared<T, VEC, UPL, BACKWARD>::warp_bytes(pairs);
+    if (BACKWARD) smem = std::max(smem, (size_t)(kRotaryThreads / 32) * c.prm.D * sizeof(float));  // the weights' sums
+    auto kernel = kla_rotary_kernel<T, VEC, UPL, NORM, BACKWARD>;
+    if (smem > 48 * 1024) {  // leave to use it, once for each device, kernel and size reached
+        static std::mutex mu;
+        static size_t allowed[256] = {};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && (dev < 0 || dev >= 256)) e = cudaErrorInvalidDevice;
+        if (e != cudaSuccess) return e;
+        std::lock_guard<std::mutex> lock(mu);
+        if (allowed[dev] < smem) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            allowed[dev] = smem;
+        }
+    }
+    kernel<<<grid, kRotaryThreads, smem, st>>>(c.prm, pairs);
     return cudaGetLastError();
 }
 
-// Rows of up to 64 VEC elements take one unit a lane, longer ones up to as
-// many as the longest row has.
+// Units a lane: one, two or four where that is enough, else as many as the
+// longest row has.
 template <typename T, int VEC, bool NORM, bool BACKWARD>
 cudaError_t launch_vec(const Call &c, cudaStream_t st) {
-    constexpr int MOST = (KLA_ROTARY_MAX_D / 2 / VEC + 31) / 32;
-    if (c.upl == 1) return launch<T, VEC, 1, NORM, BACKWARD>(c, st);
+    constexpr int MOST = KLA_ROTARY_MAX_D / (2 * VEC) / 32;
+    if constexpr (VEC > 2) {
+        if (c.upl == 1) return launch<T, VEC, 1, NORM, BACKWARD>(c, st);
+        if (c.upl == 2) return launch<T, VEC, 2, NORM, BACKWARD>(c, st);
+    }
+    if (MOST > 4 && c.upl <= 4) return launch<T, VEC, MOST < 4 ? MOST : 4, NORM, BACKWARD>(c, st);
     return launch<T, VEC, MOST, NORM, BACKWARD>(c, st);
+}
+
+template <typename T, bool NORM, bool BACKWARD>
+cudaError_t launch_type(const Call &c, cudaStream_t st) {
+    if constexpr (sizeof(T) == 2)
+        if (c.vec == 8) return launch_vec<T, 8, NORM, BACKWARD>(c, st);
+    if (c.vec == 4) return launch_vec<T, 4, NORM, BACKWARD>(c, st);
+    if (c.vec == 2) return launch_vec<T, 2, NORM, BACKWARD>(c, st);
+    return launch_vec<T, 1, NORM, BACKWARD>(c, st);
 }
 
 template <bool NORM, bool BACKWARD>
 cudaError_t launch_call(const Call &c, cudaStream_t st) {
-    if (c.dtype == KLA_F32) {
-        if (c.vec == 4) return launch_vec<float, 4, NORM, BACKWARD>(c, st);
-        if (c.vec == 2) return launch_vec<float, 2, NORM, BACKWARD>(c, st);
-        return launch_vec<float, 1, NORM, BACKWARD>(c, st);
-    }
-    if (c.vec == 8) return launch_vec<__nv_bfloat16, 8, NORM, BACKWARD>(c, st);
-    if (c.vec == 4) return launch_vec<__nv_bfloat16, 4, NORM, BACKWARD>(c, st);
-    if (c.vec == 2) return launch_vec<__nv_bfloat16, 2, NORM, BACKWARD>(c, st);
-    return launch_vec<__nv_bfloat16, 1, NORM, BACKWARD>(c, st);
+    return c.dtype == KLA_F32 ? launch_type<float, NORM, BACKWARD>(c, st)
+                              : launch_type<__nv_bfloat16, NORM, BACKWARD>(c, st);
 }
 
 // Bytes that a call's positions span.
@@ -165,9 +214,8 @@ Range positions_range(const Call &c, const int64_t *positions) {
     return range_of(positions, 8 * (n + c.T));
 }
 
-// CTAs of the backward pass: enough to fill the SMs, few enough that the
-// sums of the weights' gradients stay small.
-int64_t backward_cap() { return (int64_t)sm_count() * 4; }
+// CTAs of a backward call at most.
+int64_t backward_cap() { return (int64_t)sm_count() * KLA_ROTARY_BACKWARD_MINB; }
 
 }  // namespace
 
@@ -192,7 +240,7 @@ KLA_API kla_status_t kla_rotary_forward(const void *x, const int64_t *x_strides,
     c.prm.t[0].y = out;
     if (inverse) c.prm.sign = -1.f;
     choose_vec(&c, 1);
-    choose_blocks(&c, 1, 0);
+    choose_items(&c, 1, false);
     return launch_call<false, false>(c, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
@@ -224,7 +272,7 @@ KLA_API kla_status_t kla_qk_norm_rotary_forward(const void *q, const int64_t *q_
     c.prm.t[0].w = q_weight;
     c.prm.t[1].w = k_weight;
     choose_vec(&c, 2);
-    choose_blocks(&c, 2, 0);
+    choose_items(&c, 2, false);
     return launch_call<true, false>(c, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
@@ -283,7 +331,7 @@ KLA_API kla_status_t kla_qk_norm_rotary_backward(
     if (!do_k) t[1] = RotaryTensor{};
     if (!do_q && !do_k) return KLA_OK;
     choose_vec(&c, 2);
-    choose_blocks(&c, 2, backward_cap());
+    choose_items(&c, 2, true);
     float *partial = static_cast<float *>(workspace);
     if (do_q && grad_q_weight) t[0].partial = partial;
     if (do_k && grad_k_weight) t[1].partial = partial + (int64_t)t[0].ctas * D;
