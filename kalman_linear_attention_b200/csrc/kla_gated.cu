@@ -30,44 +30,76 @@ bool sizes(int64_t B, int64_t T, int64_t H, int64_t N, kla_gate_t gate, Sizes *s
 #define KLA_GATED_L 16
 #endif
 #ifndef KLA_GATED_BACKWARD_L
-#define KLA_GATED_BACKWARD_L 16
+#define KLA_GATED_BACKWARD_L 8
 #endif
 // Clusters are doubled while the CTAs are fewer than this many per SM.
 #ifndef KLA_GATED_FILL
 #define KLA_GATED_FILL 2
 #endif
-#ifndef KLA_GATED_VEC_F32
-#define KLA_GATED_VEC_F32 1
+#ifndef KLA_GATED_LEAST
+#define KLA_GATED_LEAST 1
 #endif
-#ifndef KLA_GATED_VEC_BF16
-#define KLA_GATED_VEC_BF16 2
+#ifndef KLA_GATED_PAIR_TILES
+#define KLA_GATED_PAIR_TILES 100
 #endif
 
 struct Launch {
     GatedTiles g;
     int64_t tiles;
-    int W, C, group;
+    int vec, W, C, group;
+    bool wide;
 };
 
-// Tiles of 32 x VEC channels.  Tiles run on over the heads of a batch row,
+// The arrays of a call: those whose rows are read through shared memory
+// (in), and those that are only written.
+struct Array {
+    const void *p;
+    int64_t size;  // of an element
+    bool in;
+};
+
+// Tiles of 32 x vec channels.  Tiles run on over the heads of a batch row,
 // unless a gate is shared by a head whose channels and a tile's do not divide
-// one another: then each head has tiles of its own, so that the sum over its
+// one another (or by heads so small that a tile has more than kGatedHeads of
+// them): then each head has tiles of its own, so that the sum over its
 // channels stays within whole tiles.
-Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, bool head, int vec, int L) {
-    Launch l;
+bool tile(int64_t B, int64_t H, int64_t N, bool head, int vec, Launch *l) {
     const int64_t cw = 32 * vec;
-    const bool own = head && N % cw != 0 && cw % N != 0;
-    l.g.T = T; l.g.H = H; l.g.N = N; l.g.HN = H * N;
-    l.g.seg = own ? N : H * N;
-    l.g.per_seg = (l.g.seg + cw - 1) / cw;
-    l.g.per_row = l.g.per_seg * (own ? H : 1);
-    l.tiles = B * l.g.per_row;
-    l.group = head && !own && N < cw ? (int)(N / vec) : 32;
-    l.W = (int)std::min<int64_t>(kGatedMaxWarps, (T + L - 1) / L);
+    const bool own = head && N % cw != 0 && (cw % N != 0 || cw / N > kGatedHeads);
+    l->vec = vec;
+    l->g.seg = own ? N : H * N;
+    l->g.per_seg = (l->g.seg + cw - 1) / cw;
+    l->g.per_row = l->g.per_seg * (own ? H : 1);
+    l->tiles = B * l->g.per_row;
+    l->group = head && !own && N < cw ? (int)(N / vec) : 32;
+    return !own;
+}
+
+// warps: how many an SM holds at once, for one and for two channels a lane.
+Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, bool head, int L, const Array *arrays, int n,
+            const int (&warps)[2]) {
+    Launch l;
+    const int64_t HN = H * N, chunks = (T + L - 1) / L;
+    l.g.T = T; l.g.H = H; l.g.N = N; l.g.HN = HN;
+    // two channels a lane where every row starts on such a pair and there are
+    // tiles enough
+    bool pairs = HN % 2 == 0 && (!head || N % 2 == 0);
+    for (int i = 0; i < n; ++i) pairs = pairs && aligned(arrays[i].p, 2 * arrays[i].size);
+    bool flat = tile(B, H, N, head, 2, &l);
+    if (!pairs || l.tiles < (int64_t)KLA_GATED_PAIR_TILES * sm_count() / 100) flat = tile(B, H, N, head, 1, &l);
+    l.wide = flat || l.g.seg % 8 == 0;
+    for (int i = 0; i < n; ++i)
+        if (arrays[i].in) l.wide = l.wide && HN * arrays[i].size % 16 == 0 && aligned(arrays[i].p, 16);
+    // few tiles: clusters, until the CTAs are KLA_GATED_FILL for each SM
     l.C = 1;
-    while (l.C < kGatedMaxCluster && l.tiles * l.C < (int64_t)KLA_GATED_FILL * sm_count() &&
-           (int64_t)l.C * l.W * L < T)
+    l.W = (int)std::min<int64_t>(kGatedMaxWarps, chunks);
+    while (l.C < kGatedMaxCluster && 2 * l.tiles * l.C <= (int64_t)KLA_GATED_FILL * sm_count() &&
+           (int64_t)l.C * l.W < chunks)
         l.C *= 2;
+    // many tiles: fewer warps each, so that all are resident at once (CTAs
+    // that had to wait for others would run alone at the end)
+    while (l.C == 1 && l.W > KLA_GATED_LEAST && l.tiles * l.W > (int64_t)warps[l.vec - 1] * sm_count())
+        l.W = (l.W + 1) / 2;
     return l;
 }
 
@@ -75,8 +107,10 @@ Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, bool head, int vec, int 
 int64_t parts_of(int64_t N, int vec) { return (N + 32 * vec - 1) / (32 * vec); }
 
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int cluster, cudaStream_t stream, A &&...args) {
+cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int cluster, size_t smem, cudaStream_t stream,
+                   A &&...args) {
     cudaLaunchConfig_t cfg = {};
+    cfg.dynamicSmemBytes = smem;
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = stream;
@@ -89,29 +123,70 @@ cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int cluster,
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-template <typename Tin, int VEC, bool HEAD>
-cudaError_t run_forward(const Launch &l, const GatedParams &prm, cudaStream_t st) {
-    constexpr int L = KLA_GATED_L;
-    return l.C > 1 ? launch(kla_gated_forward_kernel<Tin, VEC, HEAD, L, true>, l.tiles * l.C, 32 * l.W, l.C, st, prm)
-                   : launch(kla_gated_forward_kernel<Tin, VEC, HEAD, L, false>, l.tiles, 32 * l.W, 1, st, prm);
+// Leave for a kernel to use all the shared memory that its largest CTA needs,
+// once for each device.
+template <auto KERNEL>
+cudaError_t allow_smem(int smem) {
+    static std::mutex mu;
+    static bool done[256] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 256) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    done[dev] = e == cudaSuccess;
+    return e;
 }
 
-template <typename Tin, int VEC, bool HEAD>
-cudaError_t run_backward(const Launch &l, const GatedBackwardParams &prm, cudaStream_t st) {
-    constexpr int L = KLA_GATED_BACKWARD_L;
-    return l.C > 1 ? launch(kla_gated_backward_kernel<Tin, VEC, HEAD, L, true>, l.tiles * l.C, 32 * l.W, l.C, st, prm)
-                   : launch(kla_gated_backward_kernel<Tin, VEC, HEAD, L, false>, l.tiles, 32 * l.W, 1, st, prm);
+template <int VEC>
+constexpr int smem_bytes(int stage, int W, int C) {
+    return W * (stage + GatedPairs<VEC>::BYTES) + (C > 1 ? C * GatedPairs<VEC>::BYTES : 0);
 }
 
-// Channels per lane: as the type's constant says where every row of the
-// arrays (pointers `p`, of element sizes `e`; null ones are not used) starts
-// on a vector, else one.
-int vec_of(kla_dtype_t dt, int64_t HN, int64_t N, bool head, const void *const *p, const int64_t *e, int n) {
-    const int vec = dt == KLA_F32 ? KLA_GATED_VEC_F32 : KLA_GATED_VEC_BF16;
-    if (HN % vec != 0 || (head && N % vec != 0)) return 1;
-    for (int i = 0; i < n; ++i)
-        if (p[i] && !aligned(p[i], vec * e[i])) return 1;
-    return vec;
+template <auto KERNEL, int VEC, typename Params>
+cudaError_t run(const Launch &l, int stage, const Params &prm, cudaStream_t st) {
+    const cudaError_t e = allow_smem<KERNEL>(smem_bytes<VEC>(stage, kGatedMaxWarps, kGatedMaxCluster));
+    if (e != cudaSuccess) return e;
+    return launch(KERNEL, l.tiles * l.C, 32 * l.W, l.C, (size_t)smem_bytes<VEC>(stage, l.W, l.C), st, prm);
+}
+
+template <typename Tin, int VEC, bool HEAD, bool WIDE>
+cudaError_t run_scan(const Launch &l, const GatedParams &prm, cudaStream_t st) {
+    constexpr int L = KLA_GATED_L, STAGE = GatedStage<Tin, VEC, HEAD, L, false>::WARP;
+    return l.C > 1 ? run<kla_gated_forward_kernel<Tin, VEC, HEAD, L, WIDE, true>, VEC>(l, STAGE, prm, st)
+                   : run<kla_gated_forward_kernel<Tin, VEC, HEAD, L, WIDE, false>, VEC>(l, STAGE, prm, st);
+}
+template <typename Tin, int VEC, bool HEAD, bool WIDE>
+cudaError_t run_scan(const Launch &l, const GatedBackwardParams &prm, cudaStream_t st) {
+    constexpr int L = KLA_GATED_BACKWARD_L, STAGE = GatedStage<Tin, VEC, HEAD, L, true>::WARP;
+    return l.C > 1 ? run<kla_gated_backward_kernel<Tin, VEC, HEAD, L, WIDE, true>, VEC>(l, STAGE, prm, st)
+                   : run<kla_gated_backward_kernel<Tin, VEC, HEAD, L, WIDE, false>, VEC>(l, STAGE, prm, st);
+}
+template <typename Tin, int VEC, typename Params>
+cudaError_t run_vec(const Launch &l, bool head, const Params &prm, cudaStream_t st) {
+    if (head)
+        return l.wide ? run_scan<Tin, VEC, true, true>(l, prm, st) : run_scan<Tin, VEC, true, false>(l, prm, st);
+    return l.wide ? run_scan<Tin, VEC, false, true>(l, prm, st) : run_scan<Tin, VEC, false, false>(l, prm, st);
+}
+template <typename Params>
+cudaError_t run_type(const Launch &l, kla_dtype_t dt, bool head, const Params &prm, cudaStream_t st) {
+    if (dt == KLA_F32)
+        return l.vec == 2 ? run_vec<float, 2>(l, head, prm, st) : run_vec<float, 1>(l, head, prm, st);
+    return l.vec == 2 ? run_vec<__nv_bfloat16, 2>(l, head, prm, st) : run_vec<__nv_bfloat16, 1>(l, head, prm, st);
+}
+
+// Warps that an SM holds at once, by registers and by shared memory, for one
+// and for two channels a lane.
+template <typename Tin, bool BACKWARD>
+void warps_of(bool head, int (&warps)[2]) {
+    constexpr int L = BACKWARD ? KLA_GATED_BACKWARD_L : KLA_GATED_L;
+    auto fit = [](int bytes) { return std::min<int>(kGatedMaxWarps * (BACKWARD ? KLA_GATED_BACKWARD_MINB : KLA_GATED_MINB), 224 * 1024 / bytes); };
+    warps[0] = fit(smem_bytes<1>(head ? GatedStage<Tin, 1, true, L, BACKWARD>::WARP
+                                      : GatedStage<Tin, 1, false, L, BACKWARD>::WARP, 1, 1));
+    warps[1] = fit(smem_bytes<2>(head ? GatedStage<Tin, 2, true, L, BACKWARD>::WARP
+                                      : GatedStage<Tin, 2, false, L, BACKWARD>::WARP, 1, 1));
 }
 
 template <typename Tin>
@@ -158,32 +233,17 @@ KLA_API kla_status_t kla_gated_scan_forward(const void *f, const void *x, kla_dt
     const Range ins[3] = {range_of(f, e * s.gates), range_of(x, e * s.n), range_of(h0, 4 * s.C)};
     if (any_overlap(outs, 1, ins, 3)) return KLA_ERR_INVALID_ARG;
 
-    const bool head = gate == KLA_GATE_HEAD;
-    const void *p[3] = {head ? nullptr : f, x, h};
-    const int64_t es[3] = {e, e, 4};
-    const int vec = vec_of(in_dtype, s.HN, N, head, p, es, 3);
-    const Launch l = plan(B, T, H, N, head, vec, KLA_GATED_L);
+    // a gate for each head of one channel is a gate for each channel
+    const bool head = gate == KLA_GATE_HEAD && N > 1;
+    const Array arrays[3] = {{x, e, true}, {h, 4, false}, {f, e, true}};
+    int warps[2];
+    in_dtype == KLA_F32 ? warps_of<float, false>(head, warps) : warps_of<__nv_bfloat16, false>(head, warps);
+    const Launch l = plan(B, T, H, N, head, KLA_GATED_L, arrays, head ? 2 : 3, warps);
     if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
     GatedParams prm;
     prm.g = l.g;
     prm.f = f; prm.x = x; prm.h0 = h0; prm.h = h;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t err;
-    if (in_dtype == KLA_F32) {
-        if (vec == 1)
-            err = head ? run_forward<float, 1, true>(l, prm, st) : run_forward<float, 1, false>(l, prm, st);
-        else
-            err = head ? run_forward<float, KLA_GATED_VEC_F32, true>(l, prm, st)
-                       : run_forward<float, KLA_GATED_VEC_F32, false>(l, prm, st);
-    } else {
-        if (vec == 1)
-            err = head ? run_forward<__nv_bfloat16, 1, true>(l, prm, st)
-                       : run_forward<__nv_bfloat16, 1, false>(l, prm, st);
-        else
-            err = head ? run_forward<__nv_bfloat16, KLA_GATED_VEC_BF16, true>(l, prm, st)
-                       : run_forward<__nv_bfloat16, KLA_GATED_VEC_BF16, false>(l, prm, st);
-    }
-    return err == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    return run_type(l, in_dtype, head, prm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
 KLA_API kla_status_t kla_gated_scan_step(const void *f, const void *x, kla_dtype_t in_dtype, kla_gate_t gate,
@@ -251,13 +311,14 @@ KLA_API kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype
         return cudaMemsetAsync(grad_h0, 0, (size_t)(4 * s.C), st) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
     }
 
-    const bool head = gate == KLA_GATE_HEAD;
-    const void *p[5] = {head ? nullptr : f, g_h, grad_f ? h : nullptr, head ? nullptr : grad_f, grad_x};
-    const int64_t es[5] = {e, 4, 4, e, e};
-    const int vec = vec_of(in_dtype, s.HN, N, head, p, es, 5);
-    const Launch l = plan(B, T, H, N, head, vec, KLA_GATED_BACKWARD_L);
+    const bool head = gate == KLA_GATE_HEAD && N > 1;
+    const Array arrays[5] = {{g_h, 4, true}, {grad_f ? h : nullptr, 4, true}, {grad_x, e, false},
+                             {f, e, true}, {grad_f, e, false}};
+    int warps[2];
+    in_dtype == KLA_F32 ? warps_of<float, true>(head, warps) : warps_of<__nv_bfloat16, true>(head, warps);
+    const Launch l = plan(B, T, H, N, head, KLA_GATED_BACKWARD_L, arrays, head ? 3 : 5, warps);
     if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
-    const int64_t parts = head ? parts_of(N, vec) : 1;
+    const int64_t parts = head ? parts_of(N, l.vec) : 1;
     GatedBackwardParams prm;
     prm.g = l.g;
     prm.f = f; prm.h0 = h0; prm.h = h; prm.gh = g_h;
@@ -265,21 +326,7 @@ KLA_API kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype
     prm.partial = grad_f && parts > 1 ? static_cast<float *>(workspace) : nullptr;
     prm.gates = s.rows;
     prm.group = l.group;
-    cudaError_t err;
-    if (in_dtype == KLA_F32) {
-        if (vec == 1)
-            err = head ? run_backward<float, 1, true>(l, prm, st) : run_backward<float, 1, false>(l, prm, st);
-        else
-            err = head ? run_backward<float, KLA_GATED_VEC_F32, true>(l, prm, st)
-                       : run_backward<float, KLA_GATED_VEC_F32, false>(l, prm, st);
-    } else {
-        if (vec == 1)
-            err = head ? run_backward<__nv_bfloat16, 1, true>(l, prm, st)
-                       : run_backward<__nv_bfloat16, 1, false>(l, prm, st);
-        else
-            err = head ? run_backward<__nv_bfloat16, KLA_GATED_VEC_BF16, true>(l, prm, st)
-                       : run_backward<__nv_bfloat16, KLA_GATED_VEC_BF16, false>(l, prm, st);
-    }
+    cudaError_t err = run_type(l, in_dtype, head, prm, st);
     if (err == cudaSuccess && prm.partial) {
         const unsigned grid = (unsigned)std::min<int64_t>((s.rows + 255) / 256, (int64_t)sm_count() * 8);
         if (in_dtype == KLA_F32)

@@ -13,11 +13,14 @@
 // tokens: warp w of a CTA takes L consecutive tokens, each lane VEC
 // neighbouring channels.  Per round
 //
-//   1. every warp loads its L rows of f and x into registers: all the loads
-//      of the round are in flight at once, rows of 32 x VEC elements,
-//      coalesced, with no demand on alignment beyond the vector's;
-//   2. it composes them (two multiply-adds a token) and leaves (A, z) in
-//      shared memory;
+//   1. every warp asks for its rows of the next round, by asynchronous copies
+//      into shared memory (two rounds of it) of 16 bytes a lane, several rows
+//      at once (WIDE), or, where rows do not start on 16 bytes, of each lane's
+//      own channels; copies of 4 bytes a lane throughout took a third longer.
+//      Nothing waits but the warp for its own copies.  Gates shared by a head
+//      go through registers, one round ahead, a token a lane;
+//   2. it composes its tokens of this round (two multiply-adds a token) and
+//      leaves (A, z) in shared memory;
 //   3. after one barrier each warp runs through the W pairs with the state
 //      that left the previous round: the value on reaching its own pair is
 //      its entry, the last one the next round's entry;
@@ -103,31 +106,33 @@ __device__ __forceinline__ void store_remote(float2 *p, unsigned rank, float2 v)
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// The pairs (A, z) of a round, and of a cluster's CTAs; double-buffered, so
-// that one barrier a round is enough (a buffer is written again two rounds
+// The pairs (A, z) of a round's warps, and of a cluster's CTAs; double-buffered,
+// so that one barrier a round is enough (a buffer is written again two rounds
 // later, behind the barrier of the round between).
 template <int VEC>
-struct GatedShared {
-    float2 warp[2][kGatedMaxWarps][VEC][32];
-    float2 cta[2][kGatedMaxCluster][VEC][32];
+struct GatedPairs {
+    using Pairs = float2[VEC][32];
+    Pairs *warp;  // [2][W]
+    Pairs *cta;   // [2][C]
+    static constexpr int BYTES = 2 * (int)sizeof(Pairs);  // of a warp, or of a CTA of a cluster
 };
 
 // Step 2 and 3 above: leave this warp's pair, meet the others, and return
 // the state entering this warp's tokens in `entry`; `carry` goes from the
 // round's entry to its exit.  Called by all warps of the CTA (cluster).
 template <int VEC, bool CLUSTER>
-__device__ __forceinline__ void exchange(GatedShared<VEC> &sh, int buf, int w, int W, int lane, unsigned rank,
+__device__ __forceinline__ void exchange(const GatedPairs<VEC> &sh, int buf, int w, int W, int lane, unsigned rank,
                                          unsigned C, const float (&A)[VEC], const float (&z)[VEC],
                                          float (&carry)[VEC], float (&entry)[VEC]) {
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) sh.warp[buf][w][v][lane] = make_float2(A[v], z[v]);
+    for (int v = 0; v < VEC; ++v) sh.warp[buf * W + w][v][lane] = make_float2(A[v], z[v]);
     __syncthreads();
     if constexpr (!CLUSTER) {
         for (int i = 0; i < W; ++i) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 if (i == w) entry[v] = carry[v];
-                const float2 p = sh.warp[buf][i][v][lane];
+                const float2 p = sh.warp[buf * W + i][v][lane];
                 carry[v] = fmaf(p.x, carry[v], p.y);
             }
         }
@@ -145,7 +150,7 @@ __device__ __forceinline__ void exchange(GatedShared<VEC> &sh, int buf, int w, i
                     pa[v] = ta[v];
                     pz[v] = tz[v];
                 }
-                const float2 p = sh.warp[buf][i][v][lane];
+                const float2 p = sh.warp[buf * W + i][v][lane];
                 tz[v] = fmaf(p.x, tz[v], p.y);
                 ta[v] *= p.x;
             }
@@ -153,14 +158,14 @@ __device__ __forceinline__ void exchange(GatedShared<VEC> &sh, int buf, int w, i
         for (unsigned c = w; c < C; c += W)
 #pragma unroll
             for (int v = 0; v < VEC; ++v)
-                store_remote(&sh.cta[buf][rank][v][lane], c, make_float2(ta[v], tz[v]));
+                store_remote(&sh.cta[buf * C + rank][v][lane], c, make_float2(ta[v], tz[v]));
         cluster_barrier();
         float mine[VEC];
         for (unsigned c = 0; c < C; ++c) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 if (c == rank) mine[v] = carry[v];
-                const float2 p = sh.cta[buf][c][v][lane];
+                const float2 p = sh.cta[buf * C + c][v][lane];
                 carry[v] = fmaf(p.x, carry[v], p.y);
             }
         }
@@ -176,10 +181,116 @@ __device__ __forceinline__ int64_t opaque(int64_t x) {
     return x;
 }
 
-// Grid: tiles x C CTAs of 32 x W threads.
-template <typename Tin, int VEC, bool HEAD, int L, bool CLUSTER>
+// A vector on its way through shared memory: an asynchronous copy, or, for a
+// single 16-bit element, a plain one.
+template <typename T, int V>
+__device__ __forceinline__ void bring(T *to, const T *from) {
+    if constexpr (V * sizeof(T) >= 4)
+        copy_async<V * sizeof(T)>(static_cast<unsigned>(__cvta_generic_to_shared(to)), from);
+    else
+        *to = *from;
+}
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> pack_at(const T *p) {
+    return *reinterpret_cast<const Pack<T, V> *>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> pack_of(float x) {
+    Pack<T, V> p;
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.v[v] = from_float<T>(x);
+    return p;
+}
+
+// Copies of a warp's rows [0, L) x 32 VEC channels into `to`, those of them in
+// [lo, hi); row i starts at from + i * step (step is negative in reverse
+// time), at the tile's first channel; `width` channels of it are there.
+template <typename T, int VEC, int L, bool WIDE>
+__device__ __forceinline__ void bring_rows(T *to, const T *from, int64_t step, int lo, int hi, int width) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (WIDE) {
+        constexpr int E = 16 / (int)sizeof(T);      // elements a lane
+        constexpr int LANES = 32 * VEC / E;         // lanes a row
+        constexpr int ROWS = 32 / LANES;            // rows at once
+        const int col = lane % LANES * E;
+        int i = lane / LANES;
+        const T *p = from + i * step + col;
+        T *q = to + i * 32 * VEC + col;
+#pragma unroll
+        for (int k = 0; k < L / ROWS; ++k, i += ROWS, p += ROWS * step, q += ROWS * 32 * VEC)
+            if (i >= lo && i < hi && col < width) bring<T, E>(q, p);
+    } else {
+        // a lane past the last channel copies the last ones
+        const int col = lane * VEC < width ? lane * VEC : width - VEC;
+        const T *p = from + col;
+        T *q = to + lane * VEC;
+#pragma unroll
+        for (int i = 0; i < L; ++i, p += step, q += 32 * VEC)
+            if (i >= lo && i < hi) bring<T, VEC>(q, p);
+    }
+}
+
+// Gates shared by heads: those of a warp's L tokens and up to kGatedHeads heads
+// of the tile, a few in each lane, one round ahead.
+constexpr int kGatedHeads = 8;
+template <typename Tin, int L>
+struct HeadGates {
+    static constexpr int N = L * kGatedHeads / 32;
+    Tin ahead[N];
+
+    // Token i of head k: at from + i * step + k, where lo <= i < hi.
+    __device__ __forceinline__ void ask(const Tin *from, int64_t step, int heads, int lo, int hi) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int i = (n * 32 + lane) % L, k = (n * 32 + lane) / L;
+            if (n * 32 < heads * L) {  // uniform
+                ahead[n] = from_float<Tin>(1.f);
+                if (k < heads && i >= lo && i < hi) ahead[n] = from[i * step + k];
+            }
+        }
+    }
+    // Into shared memory, in fp32: [heads][L].
+    __device__ __forceinline__ void give(float *to, int heads) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (n * 32 + lane < heads * L) to[n * 32 + lane] = to_float(ahead[n]);
+    }
+};
+
+// Shared memory of a warp, in bytes: two rounds of its rows, and the gates
+// shared by heads.
+template <typename Tin, int VEC, bool HEAD, int L, bool BACKWARD>
+struct GatedStage {
+    static constexpr int X = 0;                                                  // rows of x, or of g
+    static constexpr int H = X + 32 * L * VEC * (BACKWARD ? 4 : (int)sizeof(Tin));  // rows of h
+    static constexpr int F = H + (BACKWARD ? 32 * L * VEC * 4 : 0);              // rows of f
+    static constexpr int BYTES = F + (HEAD ? 0 : 32 * L * VEC * (int)sizeof(Tin));
+    static constexpr int GATES = 2 * BYTES;
+    static constexpr int WARP = GATES + (HEAD ? L * kGatedHeads * 4 : 0);
+};
+
+// The gates of a round, by token: floats of the lane's head, or packs of the
+// rows in shared memory.  Tokens that are not there leave the state as it is.
+template <typename Tin, int VEC, bool HEAD>
+struct GateRow {
+    const float *head;  // HEAD: of the lane's head
+    const Tin *rows;    // else: of the lane's channels
+    int lo, hi;         // tokens that are there
+    __device__ __forceinline__ float at(int i, int v) const {
+        if constexpr (HEAD) return head[i];
+        return i >= lo && i < hi ? to_float(pack_at<Tin, VEC>(rows + i * 32 * VEC).v[v]) : 1.f;
+    }
+};
+
+// Grid: tiles x C CTAs of 32 x W threads.  Dynamic shared memory: GatedStage of
+// each warp, then the pairs.
+template <typename Tin, int VEC, bool HEAD, int L, bool WIDE, bool CLUSTER>
 __global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_MINB) kla_gated_forward_kernel(const GatedParams prm) {
-    __shared__ GatedShared<VEC> sh;
+    using Stage = GatedStage<Tin, VEC, HEAD, L, false>;
+    using Pairs = typename GatedPairs<VEC>::Pairs;
+    extern __shared__ __align__(16) unsigned char shared[];
     const GatedTiles &g = prm.g;
     const int lane = threadIdx.x & 31;
     const int w = threadIdx.x >> 5;
@@ -187,72 +298,84 @@ __global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_MINB) kla_gated
     const unsigned C = CLUSTER ? cluster_size() : 1u;
     const unsigned rank = CLUSTER ? cluster_rank() : 0u;
     const TileAt at = tile_at(g, blockIdx.x / C, 32 * VEC);
-    int64_t c = at.c0 + lane * VEC;
+    const int64_t c = at.c0 + lane * VEC;
     const bool valid = c < at.end;
-    if (!valid) c = at.end - VEC;  // reads a neighbour's channels, stores nothing
-    const int64_t gates = HEAD ? g.H : g.HN;
+    const int width = at.end - at.c0 < 32 * VEC ? (int)(at.end - at.c0) : 32 * VEC;
     const int64_t row0 = at.b * g.T;
-    const Tin *f = static_cast<const Tin *>(prm.f) + row0 * gates + (HEAD ? c / g.N : c);
-    const Tin *x = static_cast<const Tin *>(prm.x) + row0 * g.HN + c;
+    const int64_t head0 = HEAD ? at.c0 / g.N : 0;
+    const int heads = HEAD ? (int)((at.c0 + width - 1) / g.N - head0) + 1 : 0;
+    const Tin *f = static_cast<const Tin *>(prm.f) + (HEAD ? row0 * g.H + head0 : row0 * g.HN + at.c0);
+    const Tin *x = static_cast<const Tin *>(prm.x) + row0 * g.HN + at.c0;
     float *h = prm.h + row0 * g.HN + c;
-    constexpr int FV = HEAD ? 1 : VEC;  // gates per lane and token
+    unsigned char *const mine = shared + w * Stage::WARP;
+    float *const gates = reinterpret_cast<float *>(mine + Stage::GATES);
+    Pairs *const pairs = reinterpret_cast<Pairs *>(shared + W * Stage::WARP);
+    const GatedPairs<VEC> sh{pairs, pairs + 2 * W};
 
     float carry[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) carry[v] = prm.h0 ? prm.h0[at.b * g.HN + c + v] : 0.f;
-    if (CLUSTER) cluster_barrier();  // every rank runs before its shared memory is written
+    for (int v = 0; v < VEC; ++v) carry[v] = prm.h0 && valid ? prm.h0[at.b * g.HN + c + v] : 0.f;
 
     const int64_t span = (int64_t)W * L;
     const int64_t rounds = (g.T + span * C - 1) / (span * C);
+    HeadGates<Tin, L> ahead;
+    auto ask = [&](int64_t r) {
+        const int64_t hn = opaque(g.HN), t0 = (r * C + rank) * span + w * L;
+        const int nv = (int)(g.T - t0 < L ? g.T - t0 : L);
+        unsigned char *const to = mine + (r & 1) * Stage::BYTES;
+        bring_rows<Tin, VEC, L, WIDE>(reinterpret_cast<Tin *>(to + Stage::X), x + t0 * hn, hn, 0, nv, width);
+        if constexpr (HEAD)
+            ahead.ask(f + t0 * g.H, g.H, heads, 0, nv);
+        else
+            bring_rows<Tin, VEC, L, WIDE>(reinterpret_cast<Tin *>(to + Stage::F), f + t0 * hn, hn, 0, nv, width);
+        copies_commit();
+    };
+    ask(0);
+    if (CLUSTER) cluster_barrier();  // every rank runs before its shared memory is written
+
 #pragma unroll 1
     for (int64_t r = 0; r < rounds; ++r) {
-        const int64_t hn = opaque(g.HN), gn = HEAD ? opaque(g.H) : hn;
-        const int64_t t0 = (r * C + rank) * span + w * L;
-        const int64_t left = g.T - t0;
-        const int nv = left >= L ? L : left > 0 ? (int)left : 0;
-        Pack<Tin, FV> fr[L];
-        Pack<Tin, VEC> xr[L];
-        const Tin *ft = f + t0 * gn;
-        const Tin *xt = x + t0 * hn;
-        if (nv == L) {
-#pragma unroll
-            for (int i = 0; i < L; ++i, ft += gn, xt += hn) {
-                fr[i] = load_cs<Tin, FV>(ft);
-                xr[i] = load_cs<Tin, VEC>(xt);
-            }
-        } else {  // tokens past the end leave the state as it is: f = 1, x = 0
-#pragma unroll
-            for (int i = 0; i < L; ++i, ft += gn, xt += hn) {
-#pragma unroll
-                for (int v = 0; v < FV; ++v) fr[i].v[v] = from_float<Tin>(1.f);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) xr[i].v[v] = from_float<Tin>(0.f);
-                if (i < nv) {
-                    fr[i] = load_cs<Tin, FV>(ft);
-                    xr[i] = load_cs<Tin, VEC>(xt);
-                }
-            }
+        const int64_t hn = opaque(g.HN), t0 = (r * C + rank) * span + w * L;
+        const int nv = (int)(g.T - t0 < L ? g.T - t0 : L);
+        const unsigned char *const from = mine + (r & 1) * Stage::BYTES;
+        __syncwarp();  // the other stage and the gates have been read
+        if (HEAD) ahead.give(gates, heads);
+        if (r + 1 < rounds) {
+            ask(r + 1);
+            copies_wait<1>();
+        } else {
+            copies_wait<0>();
         }
+        __syncwarp();
+        const GateRow<Tin, VEC, HEAD> fs{gates + (HEAD && valid ? (c / g.N - head0) * L : 0),
+                                         reinterpret_cast<const Tin *>(from + Stage::F) + lane * VEC, 0, nv};
+        const Tin *const xs = reinterpret_cast<const Tin *>(from + Stage::X) + lane * VEC;
+        auto x_at = [&](int i) { return i < nv ? pack_at<Tin, VEC>(xs + i * 32 * VEC) : pack_of<Tin, VEC>(0.f); };
         float A[VEC], z[VEC], entry[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             A[v] = 1.f;
             z[v] = 0.f;
+        }
 #pragma unroll
-            for (int i = 0; i < L; ++i) {
-                const float fv = to_float(fr[i].v[HEAD ? 0 : v]);
+        for (int i = 0; i < L; ++i) {
+            const Pack<Tin, VEC> xi = x_at(i);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float fv = fs.at(i, v);
                 A[v] *= fv;
-                z[v] = fmaf(fv, z[v], to_float(xr[i].v[v]));
+                z[v] = fmaf(fv, z[v], to_float(xi.v[v]));
             }
         }
         exchange<VEC, CLUSTER>(sh, (int)(r & 1), w, W, lane, rank, C, A, z, carry, entry);
         float *ht = h + t0 * hn;
 #pragma unroll
         for (int i = 0; i < L; ++i, ht += hn) {
+            const Pack<Tin, VEC> xi = x_at(i);
             Pack<float, VEC> o;
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                entry[v] = fmaf(to_float(fr[i].v[HEAD ? 0 : v]), entry[v], to_float(xr[i].v[v]));
+                entry[v] = fmaf(fs.at(i, v), entry[v], to_float(xi.v[v]));
                 o.v[v] = entry[v];
             }
             if (valid && i < nv) store_cs<float, VEC>(ht, o);
@@ -271,137 +394,192 @@ struct GatedBackwardParams {
     int group;       // lanes that share a head (HEAD): 32, or N / VEC below it
 };
 
+// Sums of L values over the lanes of groups of `group` lanes (a power of two),
+// in a fixed order: halves of the values change hands at each step, so that
+// every lane ends with the sums of its own share of them.
+template <int L>
+struct GroupSums {
+    float x[L];
+    int first;  // this lane's share: values first .. first + count - 1
+    int count;
+    bool writes;  // among the lanes with the same share, the one that writes
+
+    __device__ __forceinline__ void run(int group) {
+        const int lane = threadIdx.x & 31;
+        first = 0;
+        count = L;
+        writes = true;
+#pragma unroll
+        for (int k = 0; k < 5; ++k) {
+            const int o = group >> (k + 1);
+            if (o == 0) continue;
+            const bool up = lane & o;
+            const int half = (L >> k) >> 1;
+            if (half > 0) {
+#pragma unroll
+                for (int j = 0; j < half; ++j) {
+                    const float give = up ? x[j] : x[half + j];
+                    const float keep = up ? x[half + j] : x[j];
+                    x[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+                first += up ? half : 0;
+                count = half;
+            } else {
+                x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+                writes = writes && !up;
+            }
+        }
+    }
+};
+
 // Grid: tiles x C CTAs of 32 x W threads; token s of the kernel is T-1-s.
-template <typename Tin, int VEC, bool HEAD, int L, bool CLUSTER>
-__global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_BACKWARD_MINB) kla_gated_backward_kernel(const GatedBackwardParams prm) {
-    __shared__ GatedShared<VEC> sh;
+// Dynamic shared memory as in the forward kernel.
+template <typename Tin, int VEC, bool HEAD, int L, bool WIDE, bool CLUSTER>
+__global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_BACKWARD_MINB)
+kla_gated_backward_kernel(const GatedBackwardParams prm) {
+    using Stage = GatedStage<Tin, VEC, HEAD, L, true>;
+    using Pairs = typename GatedPairs<VEC>::Pairs;
+    extern __shared__ __align__(16) unsigned char shared[];
     const GatedTiles &g = prm.g;
     const int lane = threadIdx.x & 31;
     const int w = threadIdx.x >> 5;
     const int W = blockDim.x >> 5;
     const unsigned C = CLUSTER ? cluster_size() : 1u;
     const unsigned rank = CLUSTER ? cluster_rank() : 0u;
-    const int64_t tile = blockIdx.x / C;
-    const TileAt at = tile_at(g, tile, 32 * VEC);
-    int64_t c = at.c0 + lane * VEC;
+    const TileAt at = tile_at(g, blockIdx.x / C, 32 * VEC);
+    const int64_t c = at.c0 + lane * VEC;
     const bool valid = c < at.end;
-    if (!valid) c = at.end - VEC;
-    const int64_t gates = HEAD ? g.H : g.HN;
+    const int width = at.end - at.c0 < 32 * VEC ? (int)(at.end - at.c0) : 32 * VEC;
     const int64_t row0 = at.b * g.T;
-    const int64_t head = HEAD ? c / g.N : 0;
-    const Tin *f = static_cast<const Tin *>(prm.f) + row0 * gates + (HEAD ? head : c);
-    const float *gh = prm.gh + row0 * g.HN + c;
-    const float *h = prm.gf ? prm.h + row0 * g.HN + c : nullptr;
-    const float *h0 = prm.h0 ? prm.h0 + at.b * g.HN + c : nullptr;
+    const int64_t head0 = HEAD ? at.c0 / g.N : 0;
+    const int heads = HEAD ? (int)((at.c0 + width - 1) / g.N - head0) + 1 : 0;
+    const Tin *f = static_cast<const Tin *>(prm.f) + (HEAD ? row0 * g.H + head0 : row0 * g.HN + at.c0);
+    const float *gh = prm.gh + row0 * g.HN + at.c0;
+    const float *h = prm.gf ? prm.h + row0 * g.HN + at.c0 : nullptr;
+    const float *h0 = prm.h0 && valid ? prm.h0 + at.b * g.HN + c : nullptr;
     Tin *gx = prm.gx ? static_cast<Tin *>(prm.gx) + row0 * g.HN + c : nullptr;
-    Tin *gf = prm.gf && !HEAD ? static_cast<Tin *>(prm.gf) + row0 * gates + c : nullptr;
-    constexpr int FV = HEAD ? 1 : VEC;
+    Tin *gf = prm.gf && !HEAD ? static_cast<Tin *>(prm.gf) + row0 * g.HN + c : nullptr;
+    unsigned char *const mine = shared + w * Stage::WARP;
+    float *const gates = reinterpret_cast<float *>(mine + Stage::GATES);
+    Pairs *const pairs = reinterpret_cast<Pairs *>(shared + W * Stage::WARP);
+    const GatedPairs<VEC> sh{pairs, pairs + 2 * W};
 
     float carry[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) carry[v] = 0.f;
-    if (CLUSTER) cluster_barrier();
 
     const int64_t span = (int64_t)W * L;
     const int64_t rounds = (g.T + span * C - 1) / (span * C);
+    HeadGates<Tin, L> ahead;
+    // of token t: g; h of token t - 1 (none before the first); f of token t + 1
+    // (none after the last)
+    auto ask = [&](int64_t r) {
+        const int64_t hn = opaque(g.HN), s0 = (r * C + rank) * span + w * L;
+        const int nv = (int)(g.T - s0 < L ? g.T - s0 : L);
+        const int64_t tl = g.T - 1 - s0;  // the chunk's last token; it walks down
+        unsigned char *const to = mine + (r & 1) * Stage::BYTES;
+        bring_rows<float, VEC, L, WIDE>(reinterpret_cast<float *>(to + Stage::X), gh + tl * hn, -hn, 0, nv, width);
+        if (h)
+            bring_rows<float, VEC, L, WIDE>(reinterpret_cast<float *>(to + Stage::H), h + (tl - 1) * hn, -hn, 0,
+                                            tl < nv ? (int)tl : nv, width);
+        if constexpr (HEAD)
+            ahead.ask(f + (tl + 1) * g.H, -g.H, heads, s0 > 0 ? 0 : 1, nv);
+        else
+            bring_rows<Tin, VEC, L, WIDE>(reinterpret_cast<Tin *>(to + Stage::F), f + (tl + 1) * hn, -hn,
+                                          s0 > 0 ? 0 : 1, nv, width);
+        copies_commit();
+    };
+    ask(0);
+    if (CLUSTER) cluster_barrier();
+
 #pragma unroll 1
     for (int64_t r = 0; r < rounds; ++r) {
-        const int64_t hn = opaque(g.HN), gn = HEAD ? opaque(g.H) : hn;
-        const int64_t s0 = (r * C + rank) * span + w * L;
-        const int64_t left = g.T - s0;
-        const int nv = left >= L ? L : left > 0 ? (int)left : 0;
-        const int64_t tl = g.T - 1 - s0;  // the chunk's last token; it walks down to tl - nv + 1
-        Pack<Tin, FV> fr[L];              // f of token t + 1
-        Pack<float, VEC> gr[L], hr[L];    // g of token t, h of token t - 1
-        const Tin *ft = f + (tl + 1) * gn;
-        const float *gt = gh + tl * hn;
-        const float *ht = h + (tl - 1) * hn;
-        if (nv == L && s0 > 0 && tl >= L) {  // every shifted row exists
-#pragma unroll
-            for (int i = 0; i < L; ++i, ft -= gn, gt -= hn, ht -= hn) {
-                fr[i] = load_cs<Tin, FV>(ft);
-                gr[i] = load_cs<float, VEC>(gt);
-                if (h) hr[i] = load_cs<float, VEC>(ht);
-            }
+        const int64_t hn = opaque(g.HN), s0 = (r * C + rank) * span + w * L;
+        const int nv = (int)(g.T - s0 < L ? g.T - s0 : L);
+        const int64_t tl = g.T - 1 - s0;
+        const unsigned char *const from = mine + (r & 1) * Stage::BYTES;
+        __syncwarp();  // the other stage and the gates have been read
+        if (HEAD) ahead.give(gates, heads);
+        if (r + 1 < rounds) {
+            ask(r + 1);
+            copies_wait<1>();
         } else {
-#pragma unroll
-            for (int i = 0; i < L; ++i, ft -= gn, gt -= hn, ht -= hn) {
-                const int64_t t = tl - i;
-                const bool on = i < nv;
-#pragma unroll
-                for (int v = 0; v < FV; ++v) fr[i].v[v] = from_float<Tin>(1.f);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) gr[i].v[v] = hr[i].v[v] = 0.f;
-                if (on && t + 1 < g.T) fr[i] = load_cs<Tin, FV>(ft);
-                if (on) gr[i] = load_cs<float, VEC>(gt);
-                if (on && h) {
-                    if (t > 0)
-                        hr[i] = load_cs<float, VEC>(ht);
-                    else if (h0)
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) hr[i].v[v] = h0[v];
-                }
-            }
+            copies_wait<0>();
         }
+        __syncwarp();
+        const GateRow<Tin, VEC, HEAD> fs{gates + (HEAD && valid ? (c / g.N - head0) * L : 0),
+                                         reinterpret_cast<const Tin *>(from + Stage::F) + lane * VEC, s0 > 0 ? 0 : 1, nv};
+        const float *const gs = reinterpret_cast<const float *>(from + Stage::X) + lane * VEC;
+        const float *const hs = reinterpret_cast<const float *>(from + Stage::H) + lane * VEC;
+        auto g_at = [&](int i) { return i < nv ? pack_at<float, VEC>(gs + i * 32 * VEC) : pack_of<float, VEC>(0.f); };
         float A[VEC], z[VEC], entry[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             A[v] = 1.f;
             z[v] = 0.f;
+        }
 #pragma unroll
-            for (int i = 0; i < L; ++i) {
-                const float fv = to_float(fr[i].v[HEAD ? 0 : v]);
+        for (int i = 0; i < L; ++i) {
+            const Pack<float, VEC> gi = g_at(i);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float fv = fs.at(i, v);
                 A[v] *= fv;
-                z[v] = fmaf(fv, z[v], gr[i].v[v]);
+                z[v] = fmaf(fv, z[v], gi.v[v]);
             }
         }
         exchange<VEC, CLUSTER>(sh, (int)(r & 1), w, W, lane, rank, C, A, z, carry, entry);
-        float sum[L];  // HEAD: this lane's share of the shared gate's gradient
+        GroupSums<L> sum;  // HEAD: this lane's share of the shared gate's gradient
         Tin *gxt = gx + tl * hn;
         Tin *gft = gf + tl * hn;
 #pragma unroll
         for (int i = 0; i < L; ++i, gxt -= hn, gft -= hn) {
+            const Pack<float, VEC> gi = g_at(i);
+            Pack<float, VEC> before = pack_of<float, VEC>(0.f);
+            if (h && i < nv) {
+                if (i < tl)
+                    before = pack_at<float, VEC>(hs + i * 32 * VEC);
+                else if (h0)
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) before.v[v] = h0[v];
+            }
             Pack<Tin, VEC> ox, of;
-            sum[i] = 0.f;
+            sum.x[i] = 0.f;
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                entry[v] = fmaf(to_float(fr[i].v[HEAD ? 0 : v]), entry[v], gr[i].v[v]);
+                entry[v] = fmaf(fs.at(i, v), entry[v], gi.v[v]);
                 ox.v[v] = from_float<Tin>(entry[v]);
                 if (HEAD)
-                    sum[i] = fmaf(entry[v], hr[i].v[v], sum[i]);
+                    sum.x[i] = fmaf(entry[v], before.v[v], sum.x[i]);
                 else
-                    of.v[v] = from_float<Tin>(entry[v] * hr[i].v[v]);
+                    of.v[v] = from_float<Tin>(entry[v] * before.v[v]);
             }
+            if (HEAD && !valid) sum.x[i] = 0.f;
             if (valid && i < nv) {
                 if (gx) store_cs<Tin, VEC>(gxt, ox);
                 if (!HEAD && gf) store_cs<Tin, VEC>(gft, of);
             }
         }
-        if (prm.gh0 && tl - nv == -1 && nv > 0 && valid) {  // this chunk ended at token 0
-            const Pack<Tin, FV> f0 = load_cs<Tin, FV>(f);
+        if (prm.gh0 && tl + 1 == nv && nv > 0 && valid) {  // this chunk ended at token 0
+            const Tin *const f0 = f + (HEAD ? c / g.N - head0 : lane * VEC);
 #pragma unroll
             for (int v = 0; v < VEC; ++v)
-                prm.gh0[at.b * g.HN + c + v] = to_float(f0.v[HEAD ? 0 : v]) * entry[v];
+                prm.gh0[at.b * g.HN + c + v] = to_float(f0[HEAD ? 0 : v]) * entry[v];
         }
         if (HEAD && prm.gf) {
-            // sum over the lanes of a head, in a fixed order
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                if (!valid) sum[i] = 0.f;
-                for (int o = prm.group >> 1; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-            }
-            const int in_group = lane & (prm.group - 1);
-            if (at.c0 + (int64_t)(lane - in_group) * VEC < at.end) {  // a head of this tile
+            sum.run(prm.group);
+            const int64_t k = at.c0 + (lane & ~(prm.group - 1)) * VEC;  // the group's first channel
+            if (k < at.end && sum.writes) {
+                const int64_t head = k / g.N;
+                const int64_t j = prm.partial ? (at.c0 - head * g.N) / (32 * VEC) : 0;
 #pragma unroll
                 for (int i = 0; i < L; ++i) {
-                    if (i >= nv || (i & (prm.group - 1)) != in_group) continue;
-                    const int64_t at_gate = (row0 + tl - i) * g.H + head;
-                    if (prm.partial) {
-                        const int64_t j = (at.c0 - head * g.N) / (32 * VEC);
-                        prm.partial[j * prm.gates + at_gate] = sum[i];
-                    } else {
-                        static_cast<Tin *>(prm.gf)[at_gate] = from_float<Tin>(sum[i]);
-                    }
+                    if (i >= sum.count || sum.first + i >= nv) continue;
+                    const int64_t at_gate = (row0 + tl - sum.first - i) * g.H + head;
+                    if (prm.partial)
+                        prm.partial[j * prm.gates + at_gate] = sum.x[i];
+                    else
+                        static_cast<Tin *>(prm.gf)[at_gate] = from_float<Tin>(sum.x[i]);
                 }
             }
         }

@@ -103,4 +103,17 @@ __device__ __forceinline__ void store_cs(T *p, const Pack<T, V> &x) {
     __stcs(reinterpret_cast<R *>(p), *reinterpret_cast<const R *>(&x));
 }
 
+// Asynchronous copy of BYTES (4, 8 or 16) to the shared-memory address `at`.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(unsigned at, const void *from) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 }  // namespace kla_mixer
