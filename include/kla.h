@@ -546,8 +546,8 @@ kla_status_t kla_gated_scan_step(const void *f, const void *x, kla_dtype_t in_dt
 
 /*
  * Device workspace that kla_gated_scan_backward needs when grad_f is wanted,
- * written to *bytes: 0 but for gates shared by a head of more than 32
- * channels (a partial sum per token, head and 32 channels).
+ * written to *bytes: 0 but for gates shared by a head of more than 8
+ * channels (room for a partial sum per token, head and 8 channels).
  */
 kla_status_t kla_gated_scan_backward_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N,
                                                     kla_dtype_t in_dtype, kla_gate_t gate, size_t *bytes);

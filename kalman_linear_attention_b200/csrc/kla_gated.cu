@@ -36,18 +36,15 @@ bool sizes(int64_t B, int64_t T, int64_t H, int64_t N, kla_gate_t gate, Sizes *s
 #ifndef KLA_GATED_FILL
 #define KLA_GATED_FILL 2
 #endif
-#ifndef KLA_GATED_LEAST
-#define KLA_GATED_LEAST 1
-#endif
-#ifndef KLA_GATED_PAIR_TILES
-#define KLA_GATED_PAIR_TILES 100
+// Tiles, in hundredths of the SMs, that are enough without narrower ones.
+#ifndef KLA_GATED_TILES
+#define KLA_GATED_TILES 100
 #endif
 
 struct Launch {
     GatedTiles g;
     int64_t tiles;
-    int vec, W, C, group;
-    bool wide;
+    int vec, S, copy, W, C, group;
 };
 
 // The arrays of a call: those whose rows are read through shared memory
@@ -58,53 +55,69 @@ struct Array {
     bool in;
 };
 
-// Tiles of 32 x vec channels.  Tiles run on over the heads of a batch row,
+// Tiles of 32 / S x vec channels.  Tiles run on over the heads of a batch row,
 // unless a gate is shared by a head whose channels and a tile's do not divide
-// one another (or by heads so small that a tile has more than kGatedHeads of
-// them): then each head has tiles of its own, so that the sum over its
-// channels stays within whole tiles.
-bool tile(int64_t B, int64_t H, int64_t N, bool head, int vec, Launch *l) {
-    const int64_t cw = 32 * vec;
-    const bool own = head && N % cw != 0 && (cw % N != 0 || cw / N > kGatedHeads);
+// one another (or by heads so small that a tile would have more of them than
+// its warps have room for): then each head has tiles of its own, so that the
+// sum over its channels stays within whole tiles.
+void tile(int64_t B, int64_t H, int64_t N, bool head, int vec, int S, Launch *l) {
+    const int64_t cw = 32 / S * vec;
+    const bool own = head && N % cw != 0 && (cw % N != 0 || cw / N > kGatedHeads / S);
     l->vec = vec;
+    l->S = S;
     l->g.seg = own ? N : H * N;
     l->g.per_seg = (l->g.seg + cw - 1) / cw;
     l->g.per_row = l->g.per_seg * (own ? H : 1);
     l->tiles = B * l->g.per_row;
-    l->group = head && !own && N < cw ? (int)(N / vec) : 32;
-    return !own;
+    l->group = head && !own && N < cw ? (int)(N / vec) : 32 / S;
 }
 
-// warps: how many an SM holds at once, for one and for two channels a lane.
-Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, bool head, int L, const Array *arrays, int n,
-            const int (&warps)[2]) {
+// How the rows of tiles of segments of `seg` channels can be copied.
+int copy_of(int64_t HN, int64_t seg, const Array *arrays, int n) {
+    bool wide = seg == HN || seg % 8 == 0, start = true;
+    for (int i = 0; i < n; ++i)
+        if (arrays[i].in && arrays[i].p) {
+            wide = wide && HN * arrays[i].size % 16 == 0;
+            start = start && aligned(arrays[i].p, 16);
+        }
+    return start ? wide ? WIDE : SHIFT : NARROW;
+}
+
+// The widest tiles of which there are enough to fill the SMs: two channels a
+// lane (where rows start on such pairs and 16 bytes), one, or one and a warp's
+// lanes in 2 or 4 parts.  resident(vec, S, copy): warps that an SM holds.
+template <typename F>
+Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, bool head, int L, const Array *arrays, int n, F resident) {
     Launch l;
-    const int64_t HN = H * N, chunks = (T + L - 1) / L;
+    const int64_t HN = H * N, sms = sm_count();
     l.g.T = T; l.g.H = H; l.g.N = N; l.g.HN = HN;
-    // two channels a lane where every row starts on such a pair and there are
-    // tiles enough
     bool pairs = HN % 2 == 0 && (!head || N % 2 == 0);
     for (int i = 0; i < n; ++i) pairs = pairs && aligned(arrays[i].p, 2 * arrays[i].size);
-    bool flat = tile(B, H, N, head, 2, &l);
-    if (!pairs || l.tiles < (int64_t)KLA_GATED_PAIR_TILES * sm_count() / 100) flat = tile(B, H, N, head, 1, &l);
-    l.wide = flat || l.g.seg % 8 == 0;
-    for (int i = 0; i < n; ++i)
-        if (arrays[i].in) l.wide = l.wide && HN * arrays[i].size % 16 == 0 && aligned(arrays[i].p, 16);
-    // few tiles: clusters, until the CTAs are KLA_GATED_FILL for each SM
+    constexpr int kForms[4][2] = {{2, 1}, {1, 1}, {1, 2}, {1, 4}};
+    for (const auto &form : kForms) {
+        const int vec = form[0], S = form[1];
+        if (vec == 2 && !pairs) continue;
+        Launch k = l;
+        tile(B, H, N, head, vec, S, &k);
+        k.copy = copy_of(HN, k.g.seg, arrays, n);
+        if (vec == 2 && k.copy != WIDE) continue;
+        if (S > 1 && (k.copy == NARROW || (T + L - 1) / L < S)) break;
+        l = k;
+        if (l.tiles * 100 >= sms * KLA_GATED_TILES) break;
+    }
+    const int64_t chunks = (T + l.S * L - 1) / (l.S * L);  // of a warp
+    // few tiles all the same: clusters, until the CTAs are KLA_GATED_FILL for each SM
     l.C = 1;
     l.W = (int)std::min<int64_t>(kGatedMaxWarps, chunks);
-    while (l.C < kGatedMaxCluster && 2 * l.tiles * l.C <= (int64_t)KLA_GATED_FILL * sm_count() &&
-           (int64_t)l.C * l.W < chunks)
-        l.C *= 2;
+    while (l.C < kGatedMaxCluster && 2 * l.tiles * l.C <= KLA_GATED_FILL * sms && (int64_t)l.C * l.W < chunks) l.C *= 2;
     // many tiles: fewer warps each, so that all are resident at once (CTAs
     // that had to wait for others would run alone at the end)
-    while (l.C == 1 && l.W > KLA_GATED_LEAST && l.tiles * l.W > (int64_t)warps[l.vec - 1] * sm_count())
-        l.W = (l.W + 1) / 2;
+    while (l.C == 1 && l.W > 1 && l.tiles * l.W > resident(l.vec, l.S, l.copy) * sms) l.W = (l.W + 1) / 2;
     return l;
 }
 
-// Tiles of a head whose gate gradients are added up by the reduce kernel.
-int64_t parts_of(int64_t N, int vec) { return (N + 32 * vec - 1) / (32 * vec); }
+// Tiles (of cw channels) of a head whose gate gradients the reduce kernel adds up.
+int64_t parts_of(int64_t N, int cw) { return (N + cw - 1) / cw; }
 
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int cluster, size_t smem, cudaStream_t stream,
@@ -152,42 +165,49 @@ cudaError_t run(const Launch &l, int stage, const Params &prm, cudaStream_t st) 
     return launch(KERNEL, l.tiles * l.C, 32 * l.W, l.C, (size_t)smem_bytes<VEC>(stage, l.W, l.C), st, prm);
 }
 
-template <typename Tin, int VEC, bool HEAD, bool WIDE>
+template <typename Tin, int VEC, int S, bool HEAD, int COPY>
 cudaError_t run_scan(const Launch &l, const GatedParams &prm, cudaStream_t st) {
-    constexpr int L = KLA_GATED_L, STAGE = GatedStage<Tin, VEC, HEAD, L, false>::WARP;
-    return l.C > 1 ? run<kla_gated_forward_kernel<Tin, VEC, HEAD, L, WIDE, true>, VEC>(l, STAGE, prm, st)
-                   : run<kla_gated_forward_kernel<Tin, VEC, HEAD, L, WIDE, false>, VEC>(l, STAGE, prm, st);
+    constexpr int L = KLA_GATED_L, STAGE = GatedStage<Tin, VEC, S, HEAD, L, COPY, false>::WARP;
+    return run<kla_gated_forward_kernel<Tin, VEC, S, HEAD, L, COPY>, VEC>(l, STAGE, prm, st);
 }
-template <typename Tin, int VEC, bool HEAD, bool WIDE>
+template <typename Tin, int VEC, int S, bool HEAD, int COPY>
 cudaError_t run_scan(const Launch &l, const GatedBackwardParams &prm, cudaStream_t st) {
-    constexpr int L = KLA_GATED_BACKWARD_L, STAGE = GatedStage<Tin, VEC, HEAD, L, true>::WARP;
-    return l.C > 1 ? run<kla_gated_backward_kernel<Tin, VEC, HEAD, L, WIDE, true>, VEC>(l, STAGE, prm, st)
-                   : run<kla_gated_backward_kernel<Tin, VEC, HEAD, L, WIDE, false>, VEC>(l, STAGE, prm, st);
+    constexpr int L = KLA_GATED_BACKWARD_L, STAGE = GatedStage<Tin, VEC, S, HEAD, L, COPY, true>::WARP;
+    return run<kla_gated_backward_kernel<Tin, VEC, S, HEAD, L, COPY>, VEC>(l, STAGE, prm, st);
 }
-template <typename Tin, int VEC, typename Params>
-cudaError_t run_vec(const Launch &l, bool head, const Params &prm, cudaStream_t st) {
-    if (head)
-        return l.wide ? run_scan<Tin, VEC, true, true>(l, prm, st) : run_scan<Tin, VEC, true, false>(l, prm, st);
-    return l.wide ? run_scan<Tin, VEC, false, true>(l, prm, st) : run_scan<Tin, VEC, false, false>(l, prm, st);
+// The forms that plan() chooses from.
+template <typename Tin, bool HEAD, typename Params>
+cudaError_t run_form(const Launch &l, const Params &prm, cudaStream_t st) {
+    if (l.copy == NARROW) return run_scan<Tin, 1, 1, HEAD, NARROW>(l, prm, st);
+    if (l.copy == SHIFT)
+        return l.S == 1   ? run_scan<Tin, 1, 1, HEAD, SHIFT>(l, prm, st)
+               : l.S == 2 ? run_scan<Tin, 1, 2, HEAD, SHIFT>(l, prm, st)
+                          : run_scan<Tin, 1, 4, HEAD, SHIFT>(l, prm, st);
+    if (l.vec == 2) return run_scan<Tin, 2, 1, HEAD, WIDE>(l, prm, st);
+    return l.S == 1   ? run_scan<Tin, 1, 1, HEAD, WIDE>(l, prm, st)
+           : l.S == 2 ? run_scan<Tin, 1, 2, HEAD, WIDE>(l, prm, st)
+                      : run_scan<Tin, 1, 4, HEAD, WIDE>(l, prm, st);
 }
 template <typename Params>
 cudaError_t run_type(const Launch &l, kla_dtype_t dt, bool head, const Params &prm, cudaStream_t st) {
-    if (dt == KLA_F32)
-        return l.vec == 2 ? run_vec<float, 2>(l, head, prm, st) : run_vec<float, 1>(l, head, prm, st);
-    return l.vec == 2 ? run_vec<__nv_bfloat16, 2>(l, head, prm, st) : run_vec<__nv_bfloat16, 1>(l, head, prm, st);
+    if (dt == KLA_F32) return head ? run_form<float, true>(l, prm, st) : run_form<float, false>(l, prm, st);
+    return head ? run_form<__nv_bfloat16, true>(l, prm, st) : run_form<__nv_bfloat16, false>(l, prm, st);
 }
 
-// Warps that an SM holds at once, by registers and by shared memory, for one
-// and for two channels a lane.
-template <typename Tin, bool BACKWARD>
-void warps_of(bool head, int (&warps)[2]) {
-    constexpr int L = BACKWARD ? KLA_GATED_BACKWARD_L : KLA_GATED_L;
-    auto fit = [](int bytes) { return std::min<int>(kGatedMaxWarps * (BACKWARD ? KLA_GATED_BACKWARD_MINB : KLA_GATED_MINB), 224 * 1024 / bytes); };
-    warps[0] = fit(smem_bytes<1>(head ? GatedStage<Tin, 1, true, L, BACKWARD>::WARP
-                                      : GatedStage<Tin, 1, false, L, BACKWARD>::WARP, 1, 1));
-    warps[1] = fit(smem_bytes<2>(head ? GatedStage<Tin, 2, true, L, BACKWARD>::WARP
-                                      : GatedStage<Tin, 2, false, L, BACKWARD>::WARP, 1, 1));
-}
+// Warps that an SM holds at once, by registers and by shared memory (two
+// rounds of rows a warp, as GatedStage has them).
+struct Resident {
+    int64_t e;
+    bool head, backward;
+    int64_t operator()(int vec, int S, int copy) const {
+        const int64_t L = backward ? KLA_GATED_BACKWARD_L : KLA_GATED_L;
+        const int64_t pad = copy == SHIFT ? 16 : 0, cw = 32 / S * vec, apart = S > 1 ? cw : 0;
+        const int64_t wide = 2 * S * (L * (4 * cw + pad) + 4 * apart), in = 2 * S * (L * (e * cw + pad) + e * apart);
+        const int64_t bytes = (backward ? 2 * wide : in) + (head ? L * kGatedHeads * 4 : in) + 512 * vec;
+        return std::min<int64_t>(kGatedMaxWarps * (backward ? KLA_GATED_BACKWARD_MINB : KLA_GATED_MINB),
+                                 224 * 1024 / bytes);
+    }
+};
 
 template <typename Tin>
 int step_vec(const GatedStepParams &prm, bool head) {
@@ -236,13 +256,11 @@ KLA_API kla_status_t kla_gated_scan_forward(const void *f, const void *x, kla_dt
     // a gate for each head of one channel is a gate for each channel
     const bool head = gate == KLA_GATE_HEAD && N > 1;
     const Array arrays[3] = {{x, e, true}, {h, 4, false}, {f, e, true}};
-    int warps[2];
-    in_dtype == KLA_F32 ? warps_of<float, false>(head, warps) : warps_of<__nv_bfloat16, false>(head, warps);
-    const Launch l = plan(B, T, H, N, head, KLA_GATED_L, arrays, head ? 2 : 3, warps);
+    const Launch l = plan(B, T, H, N, head, KLA_GATED_L, arrays, head ? 2 : 3, Resident{e, head, false});
     if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
     GatedParams prm;
     prm.g = l.g;
-    prm.f = f; prm.x = x; prm.h0 = h0; prm.h = h;
+    prm.f = f; prm.x = x; prm.h0 = h0; prm.h = h; prm.n = s.n;
     return run_type(l, in_dtype, head, prm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
@@ -278,7 +296,7 @@ KLA_API kla_status_t kla_gated_scan_backward_workspace_size(int64_t B, int64_t T
     if (!sizes(B, T, H, N, gate, &s)) return KLA_ERR_INVALID_ARG;
     *bytes = 0;
     if (gate == KLA_GATE_HEAD && s.n > 0) {
-        const int64_t parts = parts_of(N, 1);  // the narrowest tiles
+        const int64_t parts = parts_of(N, 8);  // the narrowest tiles
         if (parts > 1) *bytes = (size_t)(4 * parts * s.rows);
     }
     return KLA_OK;
@@ -314,17 +332,16 @@ KLA_API kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype
     const bool head = gate == KLA_GATE_HEAD && N > 1;
     const Array arrays[5] = {{g_h, 4, true}, {grad_f ? h : nullptr, 4, true}, {grad_x, e, false},
                              {f, e, true}, {grad_f, e, false}};
-    int warps[2];
-    in_dtype == KLA_F32 ? warps_of<float, true>(head, warps) : warps_of<__nv_bfloat16, true>(head, warps);
-    const Launch l = plan(B, T, H, N, head, KLA_GATED_BACKWARD_L, arrays, head ? 3 : 5, warps);
+    const Launch l = plan(B, T, H, N, head, KLA_GATED_BACKWARD_L, arrays, head ? 3 : 5, Resident{e, head, true});
     if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
-    const int64_t parts = head ? parts_of(N, l.vec) : 1;
+    const int64_t parts = head ? parts_of(N, 32 / l.S * l.vec) : 1;
     GatedBackwardParams prm;
     prm.g = l.g;
     prm.f = f; prm.h0 = h0; prm.h = h; prm.gh = g_h;
     prm.gf = grad_f; prm.gx = grad_x; prm.gh0 = grad_h0;
     prm.partial = grad_f && parts > 1 ? static_cast<float *>(workspace) : nullptr;
     prm.gates = s.rows;
+    prm.n = s.n;
     prm.group = l.group;
     cudaError_t err = run_type(l, in_dtype, head, prm, st);
     if (err == cudaSuccess && prm.partial) {

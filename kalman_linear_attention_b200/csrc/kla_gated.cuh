@@ -8,17 +8,19 @@
 // tokens is summed up by the pair (A, z) = (product of gates, state left by
 // a zero entry), and the state after it is A h + z.
 //
-// A CTA (or a cluster of C CTAs) owns a tile of 32 x VEC channels of one
-// batch row for the whole sequence, and walks it in rounds of C x W x L
-// tokens: warp w of a CTA takes L consecutive tokens, each lane VEC
-// neighbouring channels.  Per round
+// A CTA (or a cluster of C CTAs) owns a tile of 32 / S x VEC channels of one
+// batch row for the whole sequence, and walks it in rounds of C x W x S x L
+// tokens: warp w of a CTA takes S L consecutive tokens, each lane L of them
+// and VEC neighbouring channels (with few channels S parts of a warp's lanes
+// take narrower rows, so that there are more tiles).  Per round
 //
 //   1. every warp asks for its rows of the next round, by asynchronous copies
-//      into shared memory (two rounds of it) of 16 bytes a lane, several rows
-//      at once (WIDE), or, where rows do not start on 16 bytes, of each lane's
-//      own channels; copies of 4 bytes a lane throughout took a third longer.
-//      Nothing waits but the warp for its own copies.  Gates shared by a head
-//      go through registers, one round ahead, a token a lane;
+//      of 16 bytes a lane into shared memory (two rounds of it), several rows
+//      at once.  Where rows do not start on 16 bytes (SHIFT) the aligned
+//      pieces around them are copied and read at an offset.  Nothing waits but
+//      the warp for its own copies.  (Copies of each lane's own 4 bytes took a
+//      third longer.)  Gates shared by a head go through registers, one round
+//      ahead, a token a lane;
 //   2. it composes its tokens of this round (two multiply-adds a token) and
 //      leaves (A, z) in shared memory;
 //   3. after one barrier each warp runs through the W pairs with the state
@@ -69,6 +71,7 @@ struct GatedParams {
     const void *f, *x;
     const float *h0;
     float *h;
+    int64_t n;  // B * T * H * N
 };
 
 // Where a tile lies: batch row, first channel, end of its segment.
@@ -117,22 +120,47 @@ struct GatedPairs {
     static constexpr int BYTES = 2 * (int)sizeof(Pairs);  // of a warp, or of a CTA of a cluster
 };
 
-// Step 2 and 3 above: leave this warp's pair, meet the others, and return
-// the state entering this warp's tokens in `entry`; `carry` goes from the
-// round's entry to its exit.  Called by all warps of the CTA (cluster).
-template <int VEC, bool CLUSTER>
-__device__ __forceinline__ void exchange(const GatedPairs<VEC> &sh, int buf, int w, int W, int lane, unsigned rank,
-                                         unsigned C, const float (&A)[VEC], const float (&z)[VEC],
-                                         float (&carry)[VEC], float (&entry)[VEC]) {
+// Steps 2 and 3 above: from every lane's pair to the state entering its
+// tokens, in `entry`; `carry` goes from the round's entry to its exit.  The S
+// parts of a warp's tokens are composed by lane exchange first.  Called by all
+// warps of the CTA (cluster).
+template <int VEC, int S>
+__device__ __forceinline__ void exchange(const GatedPairs<VEC> &sh, int buf, int w, int W, unsigned rank, unsigned C,
+                                         float (&A)[VEC], float (&z)[VEC], float (&carry)[VEC], float (&entry)[VEC]) {
+    constexpr int LW = 32 / S;
+    const int lane = threadIdx.x & 31, ch = lane % LW, sub = lane / LW;
+    float ba[VEC], bz[VEC];  // of the parts before this lane's
+    if constexpr (S > 1) {
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) sh.warp[buf * W + w][v][lane] = make_float2(A[v], z[v]);
+        for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+            for (int d = 1; d < S; d *= 2) {
+                const float pa = __shfl_up_sync(0xffffffffu, A[v], d * LW);
+                const float pz = __shfl_up_sync(0xffffffffu, z[v], d * LW);
+                if (sub >= d) {
+                    z[v] = fmaf(A[v], pz, z[v]);
+                    A[v] *= pa;
+                }
+            }
+            ba[v] = __shfl_up_sync(0xffffffffu, A[v], LW);
+            bz[v] = __shfl_up_sync(0xffffffffu, z[v], LW);
+            if (sub == 0) {
+                ba[v] = 1.f;
+                bz[v] = 0.f;
+            }
+        }
+    }
+    if (S == 1 || sub == S - 1)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) sh.warp[buf * W + w][v][ch] = make_float2(A[v], z[v]);
     __syncthreads();
-    if constexpr (!CLUSTER) {
+    if (C == 1) {
+#pragma unroll 4
         for (int i = 0; i < W; ++i) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 if (i == w) entry[v] = carry[v];
-                const float2 p = sh.warp[buf * W + i][v][lane];
+                const float2 p = sh.warp[buf * W + i][v][ch];
                 carry[v] = fmaf(p.x, carry[v], p.y);
             }
         }
@@ -140,9 +168,10 @@ __device__ __forceinline__ void exchange(const GatedPairs<VEC> &sh, int buf, int
         float pa[VEC], pz[VEC], ta[VEC], tz[VEC];  // of the warps before this one, of all
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            ta[v] = 1.f;
-            tz[v] = 0.f;
+            pa[v] = ta[v] = 1.f;
+            pz[v] = tz[v] = 0.f;
         }
+#pragma unroll 4
         for (int i = 0; i < W; ++i) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
@@ -150,28 +179,32 @@ __device__ __forceinline__ void exchange(const GatedPairs<VEC> &sh, int buf, int
                     pa[v] = ta[v];
                     pz[v] = tz[v];
                 }
-                const float2 p = sh.warp[buf * W + i][v][lane];
+                const float2 p = sh.warp[buf * W + i][v][ch];
                 tz[v] = fmaf(p.x, tz[v], p.y);
                 ta[v] *= p.x;
             }
         }
-        for (unsigned c = w; c < C; c += W)
+        if (S == 1 || sub == 0)
+            for (unsigned c = w; c < C; c += W)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                store_remote(&sh.cta[buf * C + rank][v][lane], c, make_float2(ta[v], tz[v]));
+                for (int v = 0; v < VEC; ++v)
+                    store_remote(&sh.cta[buf * C + rank][v][ch], c, make_float2(ta[v], tz[v]));
         cluster_barrier();
-        float mine[VEC];
+#pragma unroll 4
         for (unsigned c = 0; c < C; ++c) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                if (c == rank) mine[v] = carry[v];
-                const float2 p = sh.cta[buf * C + c][v][lane];
+                if (c == rank) entry[v] = carry[v];
+                const float2 p = sh.cta[buf * C + c][v][ch];
                 carry[v] = fmaf(p.x, carry[v], p.y);
             }
         }
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) entry[v] = fmaf(pa[v], mine[v], pz[v]);
+        for (int v = 0; v < VEC; ++v) entry[v] = fmaf(pa[v], entry[v], pz[v]);
     }
+    if constexpr (S > 1)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) entry[v] = fmaf(ba[v], entry[v], bz[v]);
 }
 
 // The row strides, opaque to the optimiser: it would otherwise carry a pointer
@@ -202,39 +235,87 @@ __device__ __forceinline__ Pack<T, V> pack_of(float x) {
     return p;
 }
 
-// Copies of a warp's rows [0, L) x 32 VEC channels into `to`, those of them in
-// [lo, hi); row i starts at from + i * step (step is negative in reverse
-// time), at the tile's first channel; `width` channels of it are there.
-template <typename T, int VEC, int L, bool WIDE>
-__device__ __forceinline__ void bring_rows(T *to, const T *from, int64_t step, int lo, int hi, int width) {
-    const int lane = threadIdx.x & 31;
-    if constexpr (WIDE) {
-        constexpr int E = 16 / (int)sizeof(T);      // elements a lane
-        constexpr int LANES = 32 * VEC / E;         // lanes a row
-        constexpr int ROWS = 32 / LANES;            // rows at once
-        const int col = lane % LANES * E;
-        int i = lane / LANES;
-        const T *p = from + i * step + col;
-        T *q = to + i * 32 * VEC + col;
-#pragma unroll
-        for (int k = 0; k < L / ROWS; ++k, i += ROWS, p += ROWS * step, q += ROWS * 32 * VEC)
-            if (i >= lo && i < hi && col < width) bring<T, E>(q, p);
-    } else {
-        // a lane past the last channel copies the last ones
-        const int col = lane * VEC < width ? lane * VEC : width - VEC;
-        const T *p = from + col;
-        T *q = to + lane * VEC;
-#pragma unroll
-        for (int i = 0; i < L; ++i, p += step, q += 32 * VEC)
-            if (i >= lo && i < hi) bring<T, VEC>(q, p);
-    }
-}
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
 
-// Gates shared by heads: those of a warp's L tokens and up to kGatedHeads heads
-// of the tile, a few in each lane, one round ahead.
+// How rows come to shared memory: rows that all start on 16 bytes; rows that
+// start anywhere, of an array that starts on 16 bytes; and any array (each
+// lane its own channel, 16-bit elements by plain loads).
+enum { WIDE = 0, SHIFT = 1, NARROW = 2 };
+
+// A warp's S x L rows of CW channels in shared memory.  The S parts' rows are
+// set apart by a row's width, so that lanes of different parts do not meet in
+// one bank.
+template <typename T, int S, int L, int CW, int COPY>
+struct Rows {
+    static constexpr int R = S * L;
+    static constexpr int PITCH = CW * (int)sizeof(T) + (COPY == SHIFT ? 16 : 0);  // bytes
+    static constexpr int PART = L * PITCH + (S > 1 ? CW * (int)sizeof(T) : 0);
+    static constexpr int BYTES = S * PART;
+    static __device__ __forceinline__ int at(int i) { return S == 1 ? i * PITCH : i / L * PART + i % L * PITCH; }
+
+    // Ask for rows [lo, hi) (FULL: all of them, and all channels) into `to`.
+    // Row i starts at element `first` + i * step of `base`, an array of `size`
+    // elements, and has `width` channels.
+    template <bool FULL>
+    static __device__ __forceinline__ void ask(unsigned char *to, const T *base, int64_t size, int64_t first,
+                                               int64_t step, int lo, int hi, int width) {
+        const int lane = threadIdx.x & 31;
+        if constexpr (COPY == WIDE) {
+            constexpr int E = 16 / (int)sizeof(T);  // elements a lane
+            constexpr int LANES = CW / E;           // lanes a row
+            constexpr int ROWS = 32 / LANES;        // rows at once
+            const int col = lane % LANES * E;
+            int i = lane / LANES;
+            const T *p = base + first + i * step + col;
+#pragma unroll
+            for (int k = 0; k < R / ROWS; ++k, i += ROWS, p += ROWS * step)
+                if (FULL || (i >= lo && i < hi && col < width))
+                    bring<T, E>(reinterpret_cast<T *>(to + at(i) + col * (int)sizeof(T)), p);
+        } else if constexpr (COPY == SHIFT) {
+            // pieces of 16 bytes from the one that holds the row's first
+            // element; of the array's last piece what is there
+            constexpr int E = 16 / (int)sizeof(T);
+            constexpr int PIECES = CW / E + 1;
+            constexpr int ALL = R * PIECES;
+#pragma unroll
+            for (int k = 0; k < (ALL + 31) / 32; ++k) {
+                const int n = k * 32 + lane, i = n / PIECES, piece = n % PIECES;
+                if (n >= ALL || i < lo || i >= hi) continue;
+                const int64_t first_of = first + i * step;
+                const int64_t from = first_of - (first_of & (E - 1)) + piece * E;
+                if (from >= first_of + width) continue;
+                const int64_t left = size - from;
+                copy_async_part(static_cast<unsigned>(__cvta_generic_to_shared(to + at(i) + piece * 16)), base + from,
+                                left < E ? (int)left * (int)sizeof(T) : 16);
+            }
+        } else {
+            static_assert(COPY != NARROW || CW == 32, "a channel a lane");
+            const int col = lane < width ? lane : width - 1;  // past the last channel: the last one
+            const T *p = base + first + col;
+#pragma unroll
+            for (int i = 0; i < R; ++i, p += step)
+                if (FULL || (i >= lo && i < hi)) bring<T, 1>(reinterpret_cast<T *>(to + at(i)) + lane, p);
+        }
+    }
+    // Byte offset of row i's first element from the start of its row.
+    static __device__ __forceinline__ int shift(int64_t first, int64_t step, int i) {
+        if constexpr (COPY != SHIFT) return 0;
+        constexpr int E = 16 / (int)sizeof(T);
+        return (((int)first + i * (int)step) & (E - 1)) * (int)sizeof(T);
+    }
+};
+
+// Gates shared by heads: those of a warp's R = S L tokens and up to kGatedHeads
+// / S heads of the tile, a few in each lane, one round ahead.
 constexpr int kGatedHeads = 8;
-template <typename Tin, int L>
+template <typename Tin, int S, int L>
 struct HeadGates {
+    static constexpr int R = S * L;
     static constexpr int N = L * kGatedHeads / 32;
     Tin ahead[N];
 
@@ -243,70 +324,63 @@ struct HeadGates {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int i = (n * 32 + lane) % L, k = (n * 32 + lane) / L;
-            if (n * 32 < heads * L) {  // uniform
+            const int i = (n * 32 + lane) % R, k = (n * 32 + lane) / R;
+            if (n * 32 < heads * R) {  // uniform
                 ahead[n] = from_float<Tin>(1.f);
                 if (k < heads && i >= lo && i < hi) ahead[n] = from[i * step + k];
             }
         }
     }
-    // Into shared memory, in fp32: [heads][L].
+    // Into shared memory, in fp32: [heads][R].
     __device__ __forceinline__ void give(float *to, int heads) const {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            if (n * 32 + lane < heads * L) to[n * 32 + lane] = to_float(ahead[n]);
+            if (n * 32 + lane < heads * R) to[n * 32 + lane] = to_float(ahead[n]);
     }
 };
 
 // Shared memory of a warp, in bytes: two rounds of its rows, and the gates
 // shared by heads.
-template <typename Tin, int VEC, bool HEAD, int L, bool BACKWARD>
+template <typename Tin, int VEC, int S, bool HEAD, int L, int COPY, bool BACKWARD>
 struct GatedStage {
-    static constexpr int X = 0;                                                  // rows of x, or of g
-    static constexpr int H = X + 32 * L * VEC * (BACKWARD ? 4 : (int)sizeof(Tin));  // rows of h
-    static constexpr int F = H + (BACKWARD ? 32 * L * VEC * 4 : 0);              // rows of f
-    static constexpr int BYTES = F + (HEAD ? 0 : 32 * L * VEC * (int)sizeof(Tin));
+    static constexpr int CW = 32 / S * VEC;
+    using In = Rows<Tin, S, L, CW, COPY>;
+    using Wide = Rows<float, S, L, CW, COPY>;
+    static constexpr int X = 0;                                         // rows of x, or of g
+    static constexpr int H = X + (BACKWARD ? Wide::BYTES : In::BYTES);  // rows of h
+    static constexpr int F = H + (BACKWARD ? Wide::BYTES : 0);          // rows of f
+    static constexpr int BYTES = F + (HEAD ? 0 : In::BYTES);
     static constexpr int GATES = 2 * BYTES;
     static constexpr int WARP = GATES + (HEAD ? L * kGatedHeads * 4 : 0);
-};
-
-// The gates of a round, by token: floats of the lane's head, or packs of the
-// rows in shared memory.  Tokens that are not there leave the state as it is.
-template <typename Tin, int VEC, bool HEAD>
-struct GateRow {
-    const float *head;  // HEAD: of the lane's head
-    const Tin *rows;    // else: of the lane's channels
-    int lo, hi;         // tokens that are there
-    __device__ __forceinline__ float at(int i, int v) const {
-        if constexpr (HEAD) return head[i];
-        return i >= lo && i < hi ? to_float(pack_at<Tin, VEC>(rows + i * 32 * VEC).v[v]) : 1.f;
-    }
+    static_assert(BYTES % 16 == 0 && WARP % 16 == 0, "16-byte pieces");
 };
 
 // Grid: tiles x C CTAs of 32 x W threads.  Dynamic shared memory: GatedStage of
 // each warp, then the pairs.
-template <typename Tin, int VEC, bool HEAD, int L, bool WIDE, bool CLUSTER>
+template <typename Tin, int VEC, int S, bool HEAD, int L, int COPY>
 __global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_MINB) kla_gated_forward_kernel(const GatedParams prm) {
-    using Stage = GatedStage<Tin, VEC, HEAD, L, false>;
+    using Stage = GatedStage<Tin, VEC, S, HEAD, L, COPY, false>;
+    using In = typename Stage::In;
     using Pairs = typename GatedPairs<VEC>::Pairs;
+    constexpr int LW = 32 / S, R = S * L;
     extern __shared__ __align__(16) unsigned char shared[];
     const GatedTiles &g = prm.g;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, ch = lane % LW, sub = lane / LW;
     const int w = threadIdx.x >> 5;
     const int W = blockDim.x >> 5;
-    const unsigned C = CLUSTER ? cluster_size() : 1u;
-    const unsigned rank = CLUSTER ? cluster_rank() : 0u;
-    const TileAt at = tile_at(g, blockIdx.x / C, 32 * VEC);
-    const int64_t c = at.c0 + lane * VEC;
+    const unsigned C = cluster_size();
+    const unsigned rank = cluster_rank();
+    const TileAt at = tile_at(g, blockIdx.x / C, Stage::CW);
+    const int64_t c = at.c0 + ch * VEC;
     const bool valid = c < at.end;
-    const int width = at.end - at.c0 < 32 * VEC ? (int)(at.end - at.c0) : 32 * VEC;
+    const int width = at.end - at.c0 < Stage::CW ? (int)(at.end - at.c0) : Stage::CW;
     const int64_t row0 = at.b * g.T;
     const int64_t head0 = HEAD ? at.c0 / g.N : 0;
     const int heads = HEAD ? (int)((at.c0 + width - 1) / g.N - head0) + 1 : 0;
-    const Tin *f = static_cast<const Tin *>(prm.f) + (HEAD ? row0 * g.H + head0 : row0 * g.HN + at.c0);
-    const Tin *x = static_cast<const Tin *>(prm.x) + row0 * g.HN + at.c0;
-    float *h = prm.h + row0 * g.HN + c;
+    const Tin *const f = static_cast<const Tin *>(prm.f);
+    const Tin *const x = static_cast<const Tin *>(prm.x);
+    float *const h = prm.h + row0 * g.HN + c;
     unsigned char *const mine = shared + w * Stage::WARP;
     float *const gates = reinterpret_cast<float *>(mine + Stage::GATES);
     Pairs *const pairs = reinterpret_cast<Pairs *>(shared + W * Stage::WARP);
@@ -316,28 +390,87 @@ __global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_MINB) kla_gated
 #pragma unroll
     for (int v = 0; v < VEC; ++v) carry[v] = prm.h0 && valid ? prm.h0[at.b * g.HN + c + v] : 0.f;
 
-    const int64_t span = (int64_t)W * L;
+    const int64_t span = (int64_t)W * R;
     const int64_t rounds = (g.T + span * C - 1) / (span * C);
-    HeadGates<Tin, L> ahead;
-    auto ask = [&](int64_t r) {
-        const int64_t hn = opaque(g.HN), t0 = (r * C + rank) * span + w * L;
-        const int nv = (int)(g.T - t0 < L ? g.T - t0 : L);
+    HeadGates<Tin, S, L> ahead;
+    auto ask_rows = [&](auto full, int64_t r) {
+        constexpr bool FULL = decltype(full)::value;
+        const int64_t hn = opaque(g.HN), t0 = (r * C + rank) * span + w * R;
+        const int nv = FULL ? R : (int)(g.T - t0 < R ? g.T - t0 : R);
         unsigned char *const to = mine + (r & 1) * Stage::BYTES;
-        bring_rows<Tin, VEC, L, WIDE>(reinterpret_cast<Tin *>(to + Stage::X), x + t0 * hn, hn, 0, nv, width);
+        const int64_t first = (row0 + t0) * hn + at.c0;
+        In::template ask<FULL>(to + Stage::X, x, prm.n, first, hn, 0, nv, width);
         if constexpr (HEAD)
-            ahead.ask(f + t0 * g.H, g.H, heads, 0, nv);
+            ahead.ask(f + (row0 + t0) * g.H + head0, g.H, heads, 0, nv);
         else
-            bring_rows<Tin, VEC, L, WIDE>(reinterpret_cast<Tin *>(to + Stage::F), f + t0 * hn, hn, 0, nv, width);
+            In::template ask<FULL>(to + Stage::F, f, prm.n, first, hn, 0, nv, width);
         copies_commit();
     };
-    ask(0);
-    if (CLUSTER) cluster_barrier();  // every rank runs before its shared memory is written
+    // FULL rounds of a warp, all of whose tokens and channels are there, take
+    // code without their tests (a third of the instructions)
+    auto full = [&](int64_t r) { return (r * C + rank) * span + w * R + R <= g.T && width == Stage::CW; };
+    auto ask = [&](int64_t r) { full(r) ? ask_rows(Yes{}, r) : ask_rows(No{}, r); };
+    auto run = [&](auto full_, int64_t r) {
+        constexpr bool FULL = decltype(full_)::value;
+        const int64_t hn = opaque(g.HN), t0 = (r * C + rank) * span + w * R;
+        const int64_t left = g.T - t0 - sub * L;  // of this lane's tokens
+        const int nv = FULL ? L : (int)(left < L ? left : L);
+        const unsigned char *const from = mine + (r & 1) * Stage::BYTES;
+        // tokens that are not there leave the state as it is: f = 1, x = 0
+        const int64_t first = (row0 + t0) * hn + at.c0;
+        const int at_lane = sub * In::PART + ch * VEC * (int)sizeof(Tin);
+        [[maybe_unused]] const float *const gate = gates + (HEAD && valid ? (c / g.N - head0) * R : 0) + sub * L;
+        auto pack = [&](int part, int i) {
+            return pack_at<Tin, VEC>(reinterpret_cast<const Tin *>(from + part + at_lane + i * In::PITCH +
+                                                                   In::shift(first, hn, sub * L + i)));
+        };
+        auto x_at = [&](int i) { return FULL || i < nv ? pack(Stage::X, i) : pack_of<Tin, VEC>(0.f); };
+        auto f_at = [&](int i, float (&to)[VEC]) {
+            if constexpr (HEAD) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) to[v] = pack_at<float, 4>(gate + i / 4 * 4).v[i % 4];
+            } else {
+                const Pack<Tin, VEC> p = FULL || i < nv ? pack(Stage::F, i) : pack_of<Tin, VEC>(1.f);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) to[v] = to_float(p.v[v]);
+            }
+        };
+        float A[VEC], z[VEC], entry[VEC], fi[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            A[v] = 1.f;
+            z[v] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const Pack<Tin, VEC> xi = x_at(i);
+            f_at(i, fi);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                A[v] *= fi[v];
+                z[v] = fmaf(fi[v], z[v], to_float(xi.v[v]));
+            }
+        }
+        exchange<VEC, S>(sh, (int)(r & 1), w, W, rank, C, A, z, carry, entry);
+        float *ht = h + (t0 + sub * L) * hn;
+#pragma unroll
+        for (int i = 0; i < L; ++i, ht += hn) {
+            const Pack<Tin, VEC> xi = x_at(i);
+            f_at(i, fi);
+            Pack<float, VEC> o;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                entry[v] = fmaf(fi[v], entry[v], to_float(xi.v[v]));
+                o.v[v] = entry[v];
+            }
+            if (FULL || (valid && i < nv)) store_cs<float, VEC>(ht, o);
+        }
+    };
 
+    ask(0);
+    if (C > 1) cluster_barrier();  // every rank runs before its shared memory is written
 #pragma unroll 1
     for (int64_t r = 0; r < rounds; ++r) {
-        const int64_t hn = opaque(g.HN), t0 = (r * C + rank) * span + w * L;
-        const int nv = (int)(g.T - t0 < L ? g.T - t0 : L);
-        const unsigned char *const from = mine + (r & 1) * Stage::BYTES;
         __syncwarp();  // the other stage and the gates have been read
         if (HEAD) ahead.give(gates, heads);
         if (r + 1 < rounds) {
@@ -347,39 +480,7 @@ __global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_MINB) kla_gated
             copies_wait<0>();
         }
         __syncwarp();
-        const GateRow<Tin, VEC, HEAD> fs{gates + (HEAD && valid ? (c / g.N - head0) * L : 0),
-                                         reinterpret_cast<const Tin *>(from + Stage::F) + lane * VEC, 0, nv};
-        const Tin *const xs = reinterpret_cast<const Tin *>(from + Stage::X) + lane * VEC;
-        auto x_at = [&](int i) { return i < nv ? pack_at<Tin, VEC>(xs + i * 32 * VEC) : pack_of<Tin, VEC>(0.f); };
-        float A[VEC], z[VEC], entry[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            A[v] = 1.f;
-            z[v] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const Pack<Tin, VEC> xi = x_at(i);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float fv = fs.at(i, v);
-                A[v] *= fv;
-                z[v] = fmaf(fv, z[v], to_float(xi.v[v]));
-            }
-        }
-        exchange<VEC, CLUSTER>(sh, (int)(r & 1), w, W, lane, rank, C, A, z, carry, entry);
-        float *ht = h + t0 * hn;
-#pragma unroll
-        for (int i = 0; i < L; ++i, ht += hn) {
-            const Pack<Tin, VEC> xi = x_at(i);
-            Pack<float, VEC> o;
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                entry[v] = fmaf(fs.at(i, v), entry[v], to_float(xi.v[v]));
-                o.v[v] = entry[v];
-            }
-            if (valid && i < nv) store_cs<float, VEC>(ht, o);
-        }
+        full(r) ? run(Yes{}, r) : run(No{}, r);
     }
 }
 
@@ -391,7 +492,8 @@ struct GatedBackwardParams {
     float *gh0;
     float *partial;  // [tiles of a head][B, T, H]: sums over a tile, where a head has several
     int64_t gates;   // B * T * H
-    int group;       // lanes that share a head (HEAD): 32, or N / VEC below it
+    int64_t n;       // B * T * H * N
+    int group;       // lanes that share a head (HEAD): 32 / S, or N / VEC below it
 };
 
 // Sums of L values over the lanes of groups of `group` lanes (a power of two),
@@ -434,31 +536,33 @@ struct GroupSums {
 
 // Grid: tiles x C CTAs of 32 x W threads; token s of the kernel is T-1-s.
 // Dynamic shared memory as in the forward kernel.
-template <typename Tin, int VEC, bool HEAD, int L, bool WIDE, bool CLUSTER>
+template <typename Tin, int VEC, int S, bool HEAD, int L, int COPY>
 __global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_BACKWARD_MINB)
 kla_gated_backward_kernel(const GatedBackwardParams prm) {
-    using Stage = GatedStage<Tin, VEC, HEAD, L, true>;
+    using Stage = GatedStage<Tin, VEC, S, HEAD, L, COPY, true>;
+    using In = typename Stage::In;
+    using Wide = typename Stage::Wide;
     using Pairs = typename GatedPairs<VEC>::Pairs;
+    constexpr int LW = 32 / S, R = S * L;
     extern __shared__ __align__(16) unsigned char shared[];
     const GatedTiles &g = prm.g;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, ch = lane % LW, sub = lane / LW;
     const int w = threadIdx.x >> 5;
     const int W = blockDim.x >> 5;
-    const unsigned C = CLUSTER ? cluster_size() : 1u;
-    const unsigned rank = CLUSTER ? cluster_rank() : 0u;
-    const TileAt at = tile_at(g, blockIdx.x / C, 32 * VEC);
-    const int64_t c = at.c0 + lane * VEC;
+    const unsigned C = cluster_size();
+    const unsigned rank = cluster_rank();
+    const TileAt at = tile_at(g, blockIdx.x / C, Stage::CW);
+    const int64_t c = at.c0 + ch * VEC;
     const bool valid = c < at.end;
-    const int width = at.end - at.c0 < 32 * VEC ? (int)(at.end - at.c0) : 32 * VEC;
+    const int width = at.end - at.c0 < Stage::CW ? (int)(at.end - at.c0) : Stage::CW;
     const int64_t row0 = at.b * g.T;
     const int64_t head0 = HEAD ? at.c0 / g.N : 0;
     const int heads = HEAD ? (int)((at.c0 + width - 1) / g.N - head0) + 1 : 0;
-    const Tin *f = static_cast<const Tin *>(prm.f) + (HEAD ? row0 * g.H + head0 : row0 * g.HN + at.c0);
-    const float *gh = prm.gh + row0 * g.HN + at.c0;
-    const float *h = prm.gf ? prm.h + row0 * g.HN + at.c0 : nullptr;
-    const float *h0 = prm.h0 && valid ? prm.h0 + at.b * g.HN + c : nullptr;
-    Tin *gx = prm.gx ? static_cast<Tin *>(prm.gx) + row0 * g.HN + c : nullptr;
-    Tin *gf = prm.gf && !HEAD ? static_cast<Tin *>(prm.gf) + row0 * g.HN + c : nullptr;
+    const Tin *const f = static_cast<const Tin *>(prm.f);
+    const float *const h = prm.gf ? prm.h : nullptr;
+    const float *const h0 = prm.h0 && valid ? prm.h0 + at.b * g.HN + c : nullptr;
+    Tin *const gx = static_cast<Tin *>(prm.gx);
+    Tin *const gf = HEAD ? nullptr : static_cast<Tin *>(prm.gf);
     unsigned char *const mine = shared + w * Stage::WARP;
     float *const gates = reinterpret_cast<float *>(mine + Stage::GATES);
     Pairs *const pairs = reinterpret_cast<Pairs *>(shared + W * Stage::WARP);
@@ -468,36 +572,143 @@ kla_gated_backward_kernel(const GatedBackwardParams prm) {
 #pragma unroll
     for (int v = 0; v < VEC; ++v) carry[v] = 0.f;
 
-    const int64_t span = (int64_t)W * L;
+    const int64_t span = (int64_t)W * R;
     const int64_t rounds = (g.T + span * C - 1) / (span * C);
-    HeadGates<Tin, L> ahead;
+    HeadGates<Tin, S, L> ahead;
     // of token t: g; h of token t - 1 (none before the first); f of token t + 1
     // (none after the last)
-    auto ask = [&](int64_t r) {
-        const int64_t hn = opaque(g.HN), s0 = (r * C + rank) * span + w * L;
-        const int nv = (int)(g.T - s0 < L ? g.T - s0 : L);
+    auto ask_rows = [&](auto full, int64_t r) {
+        constexpr bool FULL = decltype(full)::value;
+        const int64_t hn = opaque(g.HN), s0 = (r * C + rank) * span + w * R;
+        const int nv = FULL ? R : (int)(g.T - s0 < R ? g.T - s0 : R);
         const int64_t tl = g.T - 1 - s0;  // the chunk's last token; it walks down
         unsigned char *const to = mine + (r & 1) * Stage::BYTES;
-        bring_rows<float, VEC, L, WIDE>(reinterpret_cast<float *>(to + Stage::X), gh + tl * hn, -hn, 0, nv, width);
+        const int64_t first = (row0 + tl) * hn + at.c0;
+        Wide::template ask<FULL>(to + Stage::X, prm.gh, prm.n, first, -hn, 0, nv, width);
         if (h)
-            bring_rows<float, VEC, L, WIDE>(reinterpret_cast<float *>(to + Stage::H), h + (tl - 1) * hn, -hn, 0,
-                                            tl < nv ? (int)tl : nv, width);
+            Wide::template ask<FULL>(to + Stage::H, h, prm.n, first - hn, -hn, 0, tl < nv ? (int)tl : nv, width);
         if constexpr (HEAD)
-            ahead.ask(f + (tl + 1) * g.H, -g.H, heads, s0 > 0 ? 0 : 1, nv);
+            ahead.ask(f + (row0 + tl + 1) * g.H + head0, -g.H, heads, s0 > 0 ? 0 : 1, nv);
         else
-            bring_rows<Tin, VEC, L, WIDE>(reinterpret_cast<Tin *>(to + Stage::F), f + (tl + 1) * hn, -hn,
-                                          s0 > 0 ? 0 : 1, nv, width);
+            In::template ask<FULL>(to + Stage::F, f, prm.n, first + hn, -hn, s0 > 0 ? 0 : 1, nv, width);
         copies_commit();
     };
-    ask(0);
-    if (CLUSTER) cluster_barrier();
+    // FULL: as in the forward kernel, with the tokens before and after
+    auto full = [&](int64_t r) {
+        const int64_t s0 = (r * C + rank) * span + w * R;
+        return s0 > 0 && s0 + R < g.T && width == Stage::CW;
+    };
+    auto ask = [&](int64_t r) { full(r) ? ask_rows(Yes{}, r) : ask_rows(No{}, r); };
+    auto run = [&](auto full_, int64_t r) {
+        constexpr bool FULL = decltype(full_)::value;
+        const int64_t hn = opaque(g.HN), s0 = (r * C + rank) * span + w * R;
+        const int64_t tl = g.T - 1 - s0 - sub * L;  // this lane's last token
+        const int nv = FULL ? L : (int)(tl + 1 < L ? tl + 1 : L);
+        const unsigned char *const from = mine + (r & 1) * Stage::BYTES;
+        const int64_t first = (row0 + g.T - 1 - s0) * hn + at.c0;
+        const int at_in = sub * In::PART + ch * VEC * (int)sizeof(Tin);
+        const int at_wide = sub * Wide::PART + ch * VEC * 4;
+        [[maybe_unused]] const float *const gate = gates + (HEAD && valid ? (c / g.N - head0) * R : 0) + sub * L;
+        auto wide = [&](int part, int64_t row, int i) {
+            return pack_at<float, VEC>(reinterpret_cast<const float *>(from + part + at_wide + i * Wide::PITCH +
+                                                                       Wide::shift(row, -hn, sub * L + i)));
+        };
+        auto g_at = [&](int i) { return FULL || i < nv ? wide(Stage::X, first, i) : pack_of<float, VEC>(0.f); };
+        auto f_at = [&](int i, float (&to)[VEC]) {
+            if constexpr (HEAD) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) to[v] = pack_at<float, 4>(gate + i / 4 * 4).v[i % 4];
+            } else {
+                Pack<Tin, VEC> p = pack_of<Tin, VEC>(1.f);
+                if (FULL || (i < nv && s0 + sub * L + i > 0))
+                    p = pack_at<Tin, VEC>(reinterpret_cast<const Tin *>(from + Stage::F + at_in + i * In::PITCH +
+                                                                        In::shift(first + hn, -hn, sub * L + i)));
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) to[v] = to_float(p.v[v]);
+            }
+        };
+        float A[VEC], z[VEC], entry[VEC], fi[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            A[v] = 1.f;
+            z[v] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const Pack<float, VEC> gi = g_at(i);
+            f_at(i, fi);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                A[v] *= fi[v];
+                z[v] = fmaf(fi[v], z[v], gi.v[v]);
+            }
+        }
+        exchange<VEC, S>(sh, (int)(r & 1), w, W, rank, C, A, z, carry, entry);
+        GroupSums<L> sum;  // HEAD: this lane's share of the shared gate's gradient
+        const int64_t out = (row0 + tl) * hn + c;
+        Tin *gxt = gx + out;
+        Tin *gft = gf + out;
+#pragma unroll
+        for (int i = 0; i < L; ++i, gxt -= hn, gft -= hn) {
+            const Pack<float, VEC> gi = g_at(i);
+            f_at(i, fi);
+            Pack<float, VEC> before = pack_of<float, VEC>(0.f);
+            if (h) {
+                if (FULL || (i < nv && i < tl))
+                    before = wide(Stage::H, first - hn, i);
+                else if (i < nv && h0)
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) before.v[v] = h0[v];
+            }
+            Pack<Tin, VEC> ox, of;
+            sum.x[i] = 0.f;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                entry[v] = fmaf(fi[v], entry[v], gi.v[v]);
+                ox.v[v] = from_float<Tin>(entry[v]);
+                if (HEAD)
+                    sum.x[i] = fmaf(entry[v], before.v[v], sum.x[i]);
+                else
+                    of.v[v] = from_float<Tin>(entry[v] * before.v[v]);
+            }
+            if (HEAD && !FULL && !valid) sum.x[i] = 0.f;
+            if (FULL || (valid && i < nv)) {
+                if (gx) store_cs<Tin, VEC>(gxt, ox);
+                if (!HEAD && gf) store_cs<Tin, VEC>(gft, of);
+            }
+        }
+        if (!FULL && prm.gh0 && nv > 0 && tl + 1 == nv && valid) {  // this lane ended at token 0
+            const Tin *const f0 = f + (HEAD ? row0 * g.H + c / g.N : row0 * g.HN + c);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                prm.gh0[at.b * g.HN + c + v] = to_float(f0[HEAD ? 0 : v]) * entry[v];
+        }
+        if (HEAD && prm.gf) {
+            sum.run(prm.group);
+            const int64_t k = at.c0 + (ch & ~(prm.group - 1)) * VEC;  // the group's first channel
+            if (sum.writes && (FULL || k < at.end)) {
+                const int64_t head = k / g.N;
+                const int64_t at_gate = (row0 + tl - sum.first) * g.H + head;
+                float *const part =
+                    prm.partial ? prm.partial + (at.c0 - head * g.N) / Stage::CW * prm.gates + at_gate : nullptr;
+                Tin *const gate_out = static_cast<Tin *>(prm.gf) + at_gate;
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    if (i >= sum.count) break;
+                    if (!FULL && sum.first + i >= nv) break;
+                    if (part)
+                        part[-i * g.H] = sum.x[i];
+                    else
+                        gate_out[-i * g.H] = from_float<Tin>(sum.x[i]);
+                }
+            }
+        }
+    };
 
+    ask(0);
+    if (C > 1) cluster_barrier();
 #pragma unroll 1
     for (int64_t r = 0; r < rounds; ++r) {
-        const int64_t hn = opaque(g.HN), s0 = (r * C + rank) * span + w * L;
-        const int nv = (int)(g.T - s0 < L ? g.T - s0 : L);
-        const int64_t tl = g.T - 1 - s0;
-        const unsigned char *const from = mine + (r & 1) * Stage::BYTES;
         __syncwarp();  // the other stage and the gates have been read
         if (HEAD) ahead.give(gates, heads);
         if (r + 1 < rounds) {
@@ -507,82 +718,7 @@ kla_gated_backward_kernel(const GatedBackwardParams prm) {
             copies_wait<0>();
         }
         __syncwarp();
-        const GateRow<Tin, VEC, HEAD> fs{gates + (HEAD && valid ? (c / g.N - head0) * L : 0),
-                                         reinterpret_cast<const Tin *>(from + Stage::F) + lane * VEC, s0 > 0 ? 0 : 1, nv};
-        const float *const gs = reinterpret_cast<const float *>(from + Stage::X) + lane * VEC;
-        const float *const hs = reinterpret_cast<const float *>(from + Stage::H) + lane * VEC;
-        auto g_at = [&](int i) { return i < nv ? pack_at<float, VEC>(gs + i * 32 * VEC) : pack_of<float, VEC>(0.f); };
-        float A[VEC], z[VEC], entry[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            A[v] = 1.f;
-            z[v] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const Pack<float, VEC> gi = g_at(i);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float fv = fs.at(i, v);
-                A[v] *= fv;
-                z[v] = fmaf(fv, z[v], gi.v[v]);
-            }
-        }
-        exchange<VEC, CLUSTER>(sh, (int)(r & 1), w, W, lane, rank, C, A, z, carry, entry);
-        GroupSums<L> sum;  // HEAD: this lane's share of the shared gate's gradient
-        Tin *gxt = gx + tl * hn;
-        Tin *gft = gf + tl * hn;
-#pragma unroll
-        for (int i = 0; i < L; ++i, gxt -= hn, gft -= hn) {
-            const Pack<float, VEC> gi = g_at(i);
-            Pack<float, VEC> before = pack_of<float, VEC>(0.f);
-            if (h && i < nv) {
-                if (i < tl)
-                    before = pack_at<float, VEC>(hs + i * 32 * VEC);
-                else if (h0)
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) before.v[v] = h0[v];
-            }
-            Pack<Tin, VEC> ox, of;
-            sum.x[i] = 0.f;
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                entry[v] = fmaf(fs.at(i, v), entry[v], gi.v[v]);
-                ox.v[v] = from_float<Tin>(entry[v]);
-                if (HEAD)
-                    sum.x[i] = fmaf(entry[v], before.v[v], sum.x[i]);
-                else
-                    of.v[v] = from_float<Tin>(entry[v] * before.v[v]);
-            }
-            if (HEAD && !valid) sum.x[i] = 0.f;
-            if (valid && i < nv) {
-                if (gx) store_cs<Tin, VEC>(gxt, ox);
-                if (!HEAD && gf) store_cs<Tin, VEC>(gft, of);
-            }
-        }
-        if (prm.gh0 && tl + 1 == nv && nv > 0 && valid) {  // this chunk ended at token 0
-            const Tin *const f0 = f + (HEAD ? c / g.N - head0 : lane * VEC);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                prm.gh0[at.b * g.HN + c + v] = to_float(f0[HEAD ? 0 : v]) * entry[v];
-        }
-        if (HEAD && prm.gf) {
-            sum.run(prm.group);
-            const int64_t k = at.c0 + (lane & ~(prm.group - 1)) * VEC;  // the group's first channel
-            if (k < at.end && sum.writes) {
-                const int64_t head = k / g.N;
-                const int64_t j = prm.partial ? (at.c0 - head * g.N) / (32 * VEC) : 0;
-#pragma unroll
-                for (int i = 0; i < L; ++i) {
-                    if (i >= sum.count || sum.first + i >= nv) continue;
-                    const int64_t at_gate = (row0 + tl - sum.first - i) * g.H + head;
-                    if (prm.partial)
-                        prm.partial[j * prm.gates + at_gate] = sum.x[i];
-                    else
-                        static_cast<Tin *>(prm.gf)[at_gate] = from_float<Tin>(sum.x[i]);
-                }
-            }
-        }
+        full(r) ? run(Yes{}, r) : run(No{}, r);
     }
 }
 

@@ -72,8 +72,8 @@ def test_backward_argument_errors(lib):
     assert bwd(*args(H=0, f=None)) == 0
     out = ctypes.c_size_t(7)
     size = lib.kla_gated_scan_backward_workspace_size
-    assert size(2, 100, 3, 64, 0, 1, ctypes.byref(out)) == 0 and out.value == 2 * 100 * 3 * 2 * 4
-    assert size(2, 100, 3, 32, 0, 1, ctypes.byref(out)) == 0 and out.value == 0
+    assert size(2, 100, 3, 64, 0, 1, ctypes.byref(out)) == 0 and out.value == 2 * 100 * 3 * 8 * 4
+    assert size(2, 100, 3, 8, 0, 1, ctypes.byref(out)) == 0 and out.value == 0
     assert size(2, 100, 3, 64, 0, 0, ctypes.byref(out)) == 0 and out.value == 0
     assert size(2, 0, 3, 64, 0, 1, ctypes.byref(out)) == 0 and out.value == 0
     assert size(-1, 1, 1, 1, 0, 0, ctypes.byref(out)) == 1

@@ -25,10 +25,12 @@ U = 2.0 ** -24
 HALF_STEP = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
 
 # B, T, H, N: one token, one warp, ragged chunks and tiles, several rounds,
-# clusters of 2 to 8 with a ragged end, heads that tiles do not divide
+# clusters of 2 to 8 with a ragged end, heads that tiles do not divide, tiles of
+# every width, rows that do not start on 16 bytes
 SHAPES = [(1, 1, 1, 1), (2, 1, 3, 5), (1, 16, 1, 32), (2, 17, 3, 24), (1, 128, 2, 64), (2, 129, 2, 50),
           (3, 300, 5, 7), (1, 1025, 1, 64), (2, 2500, 2, 128), (1, 4200, 4, 16), (40, 20, 8, 48),
-          (1, 333, 2, 200)]
+          (1, 333, 2, 200), (5, 150, 30, 32), (3, 150, 30, 32), (7, 90, 23, 31), (4, 90, 23, 31), (2, 700, 3, 11),
+          (1, 2100, 2, 13)]
 
 
 def _kla():
