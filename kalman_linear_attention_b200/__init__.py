@@ -24,5 +24,6 @@ _API_NAMES = {
 def __getattr__(name):
     if name in _API_NAMES:
         from . import api
-        return getattr(api, name)
+        globals()[name] = value = getattr(api, name)  # found directly from now on
+        return value
     raise AttributeError(name)

@@ -657,55 +657,56 @@ def scan_forward_lti(a: torch.Tensor, phi: torch.Tensor, b: torch.Tensor, lam0: 
 
 
 # ------------------------------------------------ gated linear recurrence
-class _Launch:
-    """Device, stream and allocations of one call: the work goes to ``stream``
-    (default: the current stream of the tensors' device), and what the call
-    allocates belongs to that stream, whichever one is current."""
-
-    def __init__(self, like: torch.Tensor, stream: Optional[torch.cuda.Stream]):
-        self.device = like.device
-        index = like.device.index
-        if stream is not None and stream.device.index != index:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {like.device}")
-        current = torch.cuda.current_stream(index)
-        self.handle = current.cuda_stream if stream is None else stream.cuda_stream
-        self._outer = None
-        if torch.cuda.current_device() != index or self.handle != current.cuda_stream:
-            self._outer = torch.cuda.stream(stream if stream is not None else current)
-
-    def __enter__(self) -> "_Launch":
-        if self._outer is not None:
-            self._outer.__enter__()
-        return self
-
-    def __exit__(self, *exc) -> None:
-        if self._outer is not None:
-            self._outer.__exit__(*exc)
-
-    def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
-        return torch.empty(shape, dtype=dtype, device=self.device)
+# The current stream of a device as a plain handle: constructing a
+# torch.cuda.Stream for it takes longer than the rest of a call.
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_CODES = {torch.float32: KLA_F32, torch.bfloat16: KLA_BF16}
 
 
-def _require_like(device: torch.device, **tensors: Optional[torch.Tensor]) -> None:
-    """Every tensor dense and on `device`, a CUDA device."""
-    if device.type != "cuda":
-        raise ValueError("tensor must be on a CUDA device")
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, as the other tensors are")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _enqueue(index: int, stream: Optional[torch.cuda.Stream], call):
+    """``call(handle)`` with device ``index`` current and its work on
+    ``stream`` (default: the device's current stream), so that what the call
+    allocates belongs to that stream, whichever one is current outside."""
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return call(_current_handle(index))
+        with torch.cuda.device(index):
+            return call(_current_handle(index))
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
-def _require_shape(name: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype) -> None:
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape):
+def _refuse(name: str, t: torch.Tensor, shape, dtype: torch.dtype, index: int):
+    """Why a tensor that should be dense, of this shape and type and on this
+    device is not accepted."""
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the device of the other tensors; it is on {t.device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _need(name: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, index: int) -> Optional[int]:
+    """The address of a dense tensor of this shape and type on device `index`
+    (None: of no tensor)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, index)
+    return t.data_ptr()
+
+
+def _need_workspace(t: Optional[torch.Tensor], index: int) -> Tuple[Optional[int], int]:
+    if t is None:
+        return None, 0
+    return _need("workspace", t, t.shape, t.dtype, index), t.numel() * t.element_size()
 
 
 def _gate(f: torch.Tensor, shape) -> int:
@@ -718,6 +719,15 @@ def _gate(f: torch.Tensor, shape) -> int:
                      f"got {list(f.shape)}")
 
 
+def _gates_and_inputs(f: torch.Tensor, x: torch.Tensor) -> Tuple[int, int]:
+    code = _CODES.get(x.dtype)
+    if code is None:
+        _dtype_code(x)
+    if f.dtype != x.dtype:
+        raise TypeError("f and x must share one dtype")
+    return code, _gate(f, x.shape)
+
+
 def gated_scan_forward(f: torch.Tensor, x: torch.Tensor, h0: Optional[torch.Tensor] = None, *,
                        out: Optional[torch.Tensor] = None,
                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
@@ -727,22 +737,22 @@ def gated_scan_forward(f: torch.Tensor, x: torch.Tensor, h0: Optional[torch.Tens
     [B, H, N] fp32 (None: zero).  Returns the states, fp32 [B, T, H, N]; the
     last one continues with gated_scan_step.  Enqueued on ``stream`` (default:
     the current stream) without synchronising."""
-    if x.dim() != 4:
+    shape = x.shape
+    if len(shape) != 4:
         raise ValueError("x must be [B, T, H, N]")
-    B, T, H, N = x.shape
-    gate = _gate(f, x.shape)
-    code = _dtype_code(x)
-    if f.dtype != x.dtype:
-        raise TypeError("f and x must share one dtype")
-    _require_shape("h0", h0, (B, H, N), torch.float32)
-    _require_shape("out", out, x.shape, torch.float32)
-    _require_like(x.device, f=f, x=x, h0=h0, out=out)
-    with _Launch(x, stream) as on:
-        if out is None:
-            out = on.empty(x.shape, torch.float32)
-        st = lib().kla_gated_scan_forward(_ptr(f), _ptr(x), code, gate, _ptr(h0), _ptr(out), B, T, H, N, on.handle)
-    _check(st, "kla_gated_scan_forward")
-    return out
+    B, T, H, N = shape
+    code, gate = _gates_and_inputs(f, x)
+    index = x.get_device()
+    pf, px = _need("f", f, f.shape, x.dtype, index), _need("x", x, shape, x.dtype, index)
+    ph0, ph = _need("h0", h0, (B, H, N), torch.float32, index), _need("out", out, shape, torch.float32, index)
+
+    def call(handle):
+        h = out if out is not None else torch.empty_like(x, dtype=torch.float32)
+        _check(lib().kla_gated_scan_forward(pf, px, code, gate, ph0, ph or h.data_ptr(), B, T, H, N, handle),
+               "kla_gated_scan_forward")
+        return h
+
+    return _enqueue(index, stream, call)
 
 
 def gated_scan_step(f: torch.Tensor, x: torch.Tensor, h_state: torch.Tensor, *,
@@ -751,21 +761,25 @@ def gated_scan_step(f: torch.Tensor, x: torch.Tensor, h_state: torch.Tensor, *,
     """One decode token of the gated recurrence (kla_gated_scan_step): x
     [B, H, N], f of that shape or [B, H], h_state [B, H, N] fp32.  The new state
     goes to ``out``, or in place to h_state without it; returns where it went."""
-    if x.dim() != 3:
-        raise ValueError("x must be [B, H, N]")
-    B, H, N = x.shape
-    gate = _gate(f, x.shape)
-    code = _dtype_code(x)
-    if f.dtype != x.dtype:
-        raise TypeError("f and x must share one dtype")
     if out is None:
         out = h_state
-    _require_shape("h_state", h_state, x.shape, torch.float32)
-    _require_shape("out", out, x.shape, torch.float32)
-    _require_like(x.device, f=f, x=x, h_state=h_state, out=out)
-    with _Launch(x, stream) as on:
-        st = lib().kla_gated_scan_step(_ptr(f), _ptr(x), code, gate, _ptr(h_state), _ptr(out), B, H, N, on.handle)
-    _check(st, "kla_gated_scan_step")
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    f_shape = f.shape
+    # a decode step takes a few microseconds: one test for what is as it should be
+    if (len(shape) != 3 or dtype not in _CODES or f.dtype != dtype or (f_shape != shape and f_shape != shape[:-1])
+            or h_state.shape != shape or out.shape != shape or h_state.dtype != torch.float32
+            or out.dtype != torch.float32 or f.get_device() != index or h_state.get_device() != index
+            or out.get_device() != index or not f.is_contiguous() or not x.is_contiguous()
+            or not h_state.is_contiguous() or not out.is_contiguous()):
+        if len(shape) != 3:
+            raise ValueError("x must be [B, H, N]")
+        _gates_and_inputs(f, x)
+        _need("f", f, f_shape, dtype, index), _need("x", x, shape, dtype, index)
+        _need("h_state", h_state, shape, torch.float32, index), _need("out", out, shape, torch.float32, index)
+    B, H, N = shape
+    args = (f.data_ptr(), x.data_ptr(), _CODES[dtype], KLA_GATE_CHANNEL if f_shape == shape else KLA_GATE_HEAD,
+            h_state.data_ptr(), out.data_ptr(), B, H, N)
+    _check(_enqueue(index, stream, lambda handle: lib().kla_gated_scan_step(*args, handle)), "kla_gated_scan_step")
     return out
 
 
@@ -786,27 +800,31 @@ def gated_scan_backward(f: torch.Tensor, h: torch.Tensor, g_h: torch.Tensor, h0:
     h0 as given to it, h the states it returned, g_h the loss gradient with
     respect to them (fp32).  Returns the gradients with respect to (f, x, h0):
     the first two in f's dtype, the last fp32; None where ``want`` is False."""
-    if h.dim() != 4:
+    shape = h.shape
+    if len(shape) != 4:
         raise ValueError("h must be the forward output, [B, T, H, N]")
-    B, T, H, N = h.shape
-    gate = _gate(f, h.shape)
+    B, T, H, N = shape
+    gate = _gate(f, shape)
     code = _dtype_code(f)
-    _require_shape("h", h, h.shape, torch.float32)
-    _require_shape("g_h", g_h, h.shape, torch.float32)
-    _require_shape("h0", h0, (B, H, N), torch.float32)
-    _require_like(h.device, f=f, h=h, g_h=g_h, h0=h0, workspace=workspace)
-    with _Launch(h, stream) as on:
-        gf = on.empty(f.shape, f.dtype) if want[0] else None
-        gx = on.empty(h.shape, f.dtype) if want[1] else None
-        gh0 = on.empty((B, H, N), torch.float32) if want[2] else None
-        if workspace is None and gate == KLA_GATE_HEAD and want[0]:
+    index = h.get_device()
+    args = (_need("f", f, f.shape, f.dtype, index), code, gate, _need("h0", h0, (B, H, N), torch.float32, index),
+            _need("h", h, shape, torch.float32, index), _need("g_h", g_h, shape, torch.float32, index))
+    pw, nw = _need_workspace(workspace, index)
+
+    def call(handle):
+        gf = torch.empty_like(f) if want[0] else None
+        gx = torch.empty_like(h, dtype=f.dtype) if want[1] else None
+        gh0 = h.new_empty((B, H, N)) if want[2] else None
+        ws, n = pw, nw
+        if ws is None and gate == KLA_GATE_HEAD and want[0]:
             n = gated_scan_backward_workspace_size(B, T, H, N, f.dtype, True)
-            workspace = on.empty(n, torch.uint8) if n else None
-        st = lib().kla_gated_scan_backward(
-            _ptr(f), code, gate, _ptr(h0), _ptr(h), _ptr(g_h), _ptr(gf), _ptr(gx), _ptr(gh0), B, T, H, N,
-            _ptr(workspace), workspace.numel() if workspace is not None else 0, on.handle)
-    _check(st, "kla_gated_scan_backward")
-    return gf, gx, gh0
+            room = torch.empty(n, dtype=torch.uint8, device=h.device) if n else None
+            ws = _ptr(room)
+        _check(lib().kla_gated_scan_backward(*args, _ptr(gf), _ptr(gx), _ptr(gh0), B, T, H, N, ws, n, handle),
+               "kla_gated_scan_backward")
+        return gf, gx, gh0
+
+    return _enqueue(index, stream, call)
 
 
 class GatedScan(torch.autograd.Function):
@@ -873,48 +891,53 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "n
     return inv_freq.to(device) if device is not None else inv_freq, scale
 
 
-def _head_rows(name: str, t: torch.Tensor, like: torch.Tensor):
+_I64x3 = ctypes.c_int64 * 3
+
+
+def _head_rows(name: str, t: torch.Tensor, dtype: torch.dtype, index: int):
     """The host array of the strides of [B, T, H, D] rows (None: dense)."""
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, as the other tensors are")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the device of the other tensors; it is on {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.is_contiguous():
         return None
     sb, st, sh, sd = t.stride()
     if sd != 1 and t.shape[3] > 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
-    return (ctypes.c_int64 * 3)(sb, st, sh)
+    return _I64x3(sb, st, sh)
 
 
-def _rotation(like: torch.Tensor, B: int, T: int, D: int, inv_freq: Optional[torch.Tensor],
+def _rotation(index: int, B: int, T: int, D: int, inv_freq: Optional[torch.Tensor],
               positions: Optional[torch.Tensor]):
     """(inv_freq pointer, rot_dim, positions pointer, batch stride)."""
-    dev = like.device
     if inv_freq is None:
         if positions is not None:
             raise ValueError("positions need inv_freq")
         return None, 0, None, 0
     if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > D:
         raise ValueError(f"inv_freq must be [rot_dim / 2] with rot_dim at most {D}, got {list(inv_freq.shape)}")
-    if inv_freq.dtype != torch.float64:
-        raise TypeError(f"inv_freq must be torch.float64, got {inv_freq.dtype}")
-    _require_like(dev, inv_freq=inv_freq)
+    half = inv_freq.shape[0]
+    freq = _need("inv_freq", inv_freq, (half,), torch.float64, index)
     if positions is None:
-        return inv_freq.data_ptr(), 2 * inv_freq.shape[0], None, 0
+        return freq, 2 * half, None, 0
     if positions.dtype != torch.int64:
         raise TypeError(f"positions must be torch.int64, got {positions.dtype}")
-    if positions.device != dev:
-        raise ValueError(f"positions must be on {dev}, as the other tensors are")
-    if positions.shape == (T,):
-        batch = 0
-    elif positions.shape == (B, T):
+    if positions.get_device() != index:
+        raise ValueError(f"positions must be on the device of the other tensors; they are on {positions.device}")
+    if positions.shape == (B, T):
         batch = positions.stride(0) if B > 1 else 0
+    elif positions.shape == (T,):
+        batch = 0
     else:
         raise ValueError(f"positions must be [{B}, {T}] or [{T}], got {list(positions.shape)}")
     if T > 1 and positions.stride(-1) != 1:
         raise ValueError("the last axis of positions must be contiguous")
-    return inv_freq.data_ptr(), 2 * inv_freq.shape[0], positions.data_ptr(), batch
+    return freq, 2 * half, positions.data_ptr(), batch
+
+
+def _empty_rows(like: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def rotary_forward(x: torch.Tensor, inv_freq: torch.Tensor, positions: Optional[torch.Tensor] = None, *,
@@ -927,21 +950,23 @@ def rotary_forward(x: torch.Tensor, inv_freq: torch.Tensor, positions: Optional[
     (rotary_frequencies); positions int64 [B, T] or [T], or None for position0
     + t; ``interleaved``: neighbours form a pair, else the two halves do;
     ``inverse``: the other way round.  Returns a dense tensor of x's type."""
-    if x.dim() != 4:
+    shape = x.shape
+    if len(shape) != 4:
         raise ValueError("x must be [B, T, H, D]")
-    B, T, H, D = x.shape
+    B, T, H, D = shape
     code = _dtype_code(x)
-    strides = _head_rows("x", x, x)
-    freq, rot, pos, batch = _rotation(x, B, T, D, inv_freq, positions)
-    _require_shape("out", out, x.shape, x.dtype)
-    _require_like(x.device, out=out)
-    with _Launch(x, stream) as on:
-        if out is None:
-            out = on.empty(x.shape, x.dtype)
-        st = lib().kla_rotary_forward(_ptr(x), strides, code, freq, rot, int(interleaved), scale, int(inverse), pos,
-                                      batch, position0, _ptr(out), B, T, H, D, on.handle)
-    _check(st, "kla_rotary_forward")
-    return out
+    index = x.get_device()
+    strides = _head_rows("x", x, x.dtype, index)
+    freq, rot, pos, batch = _rotation(index, B, T, D, inv_freq, positions)
+    po = _need("out", out, shape, x.dtype, index)
+
+    def call(handle):
+        y = out if out is not None else _empty_rows(x)
+        _check(lib().kla_rotary_forward(x.data_ptr(), strides, code, freq, rot, interleaved, scale, inverse, pos, batch,
+                                        position0, po or y.data_ptr(), B, T, H, D, handle), "kla_rotary_forward")
+        return y
+
+    return _enqueue(index, stream, call)
 
 
 class Rotary(torch.autograd.Function):
@@ -966,11 +991,24 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions: Optional[torch.Te
     return Rotary.apply(x, inv_freq, positions, position0, interleaved, scale)
 
 
-def _qk_shapes(q: torch.Tensor, k: torch.Tensor) -> Tuple[int, int, int, int, int]:
-    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+def _qk_call(q: torch.Tensor, k: torch.Tensor, q_weight, k_weight, eps, inv_freq, positions, position0,
+             interleaved, scale):
+    """(device, sizes, the C arguments up to position0) of a QK-Norm call."""
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4:
         raise ValueError("q must be [B, T, Hq, D] and k [B, T, Hk, D]")
-    B, T, Hq, D = q.shape
-    return B, T, Hq, k.shape[2], D
+    B, T, Hq, D = qs
+    Bk, Tk, Hk, Dk = ks
+    if B != Bk or T != Tk or D != Dk:
+        raise ValueError("q must be [B, T, Hq, D] and k [B, T, Hk, D]")
+    dtype, index = q.dtype, q.get_device()
+    code = _dtype_code(q)
+    q_strides, k_strides = _head_rows("q", q, dtype, index), _head_rows("k", k, dtype, index)
+    freq, rot, pos, batch = _rotation(index, B, T, D, inv_freq, positions)
+    return index, (B, T, Hq, Hk, D), (
+        q.data_ptr(), q_strides, k.data_ptr(), k_strides, code,
+        _need("q_weight", q_weight, (D,), torch.float32, index),
+        _need("k_weight", k_weight, (D,), torch.float32, index), eps, freq, rot, interleaved, scale, pos, batch, position0)
 
 
 def qk_norm_rotary_forward(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
@@ -985,25 +1023,18 @@ def qk_norm_rotary_forward(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[
     RMS norm of each head, times the weight ([D] fp32 or None), rotated as in
     rotary_forward (not at all without inv_freq).  Returns dense (q, k) of the
     inputs' type."""
-    B, T, Hq, Hk, D = _qk_shapes(q, k)
-    code = _dtype_code(q)
-    qs, ks = _head_rows("q", q, q), _head_rows("k", k, q)
-    freq, rot, pos, batch = _rotation(q, B, T, D, inv_freq, positions)
-    _require_shape("q_weight", q_weight, (D,), torch.float32)
-    _require_shape("k_weight", k_weight, (D,), torch.float32)
-    _require_like(q.device, q_weight=q_weight, k_weight=k_weight)
+    index, sizes, args = _qk_call(q, k, q_weight, k_weight, eps, inv_freq, positions, position0, interleaved, scale)
     q_out, k_out = (None, None) if out is None else out
-    _require_shape("out", q_out, q.shape, q.dtype)
-    _require_shape("out", k_out, k.shape, q.dtype)
-    _require_like(q.device, q_out=q_out, k_out=k_out)
-    with _Launch(q, stream) as on:
-        if out is None:
-            q_out, k_out = on.empty(q.shape, q.dtype), on.empty(k.shape, q.dtype)
-        st = lib().kla_qk_norm_rotary_forward(
-            _ptr(q), qs, _ptr(k), ks, code, _ptr(q_weight), _ptr(k_weight), eps, freq, rot, int(interleaved), scale,
-            pos, batch, position0, _ptr(q_out), _ptr(k_out), B, T, Hq, Hk, D, on.handle)
-    _check(st, "kla_qk_norm_rotary_forward")
-    return q_out, k_out
+    pq, pk = _need("out", q_out, q.shape, q.dtype, index), _need("out", k_out, k.shape, q.dtype, index)
+
+    def call(handle):
+        yq = q_out if q_out is not None else _empty_rows(q)
+        yk = k_out if k_out is not None else _empty_rows(k)
+        _check(lib().kla_qk_norm_rotary_forward(*args, pq or yq.data_ptr(), pk or yk.data_ptr(), *sizes, handle),
+               "kla_qk_norm_rotary_forward")
+        return yq, yk
+
+    return _enqueue(index, stream, call)
 
 
 def qk_norm_rotary_backward_workspace_size(Hq: int, Hk: int, D: int) -> int:
@@ -1026,32 +1057,26 @@ def qk_norm_rotary_backward(q: torch.Tensor, k: torch.Tensor, g_q: Optional[torc
     k_weight): the first two dense in the inputs' type, the weights' fp32;
     None where ``want`` is False, where there is no weight, or where the
     output's gradient is None."""
-    B, T, Hq, Hk, D = _qk_shapes(q, k)
-    code = _dtype_code(q)
-    qs, ks = _head_rows("q", q, q), _head_rows("k", k, q)
-    freq, rot, pos, batch = _rotation(q, B, T, D, inv_freq, positions)
-    _require_shape("q_weight", q_weight, (D,), torch.float32)
-    _require_shape("k_weight", k_weight, (D,), torch.float32)
-    _require_shape("g_q", g_q, q.shape, q.dtype)
-    _require_shape("g_k", g_k, k.shape, q.dtype)
-    _require_like(q.device, q_weight=q_weight, k_weight=k_weight, g_q=g_q, g_k=g_k, workspace=workspace)
-    want = (want[0] and g_q is not None, want[1] and g_k is not None,
-            want[2] and g_q is not None and q_weight is not None,
-            want[3] and g_k is not None and k_weight is not None)
-    with _Launch(q, stream) as on:
-        gq = on.empty(q.shape, q.dtype) if want[0] else None
-        gk = on.empty(k.shape, q.dtype) if want[1] else None
-        gqw = on.empty((D,), torch.float32) if want[2] else None
-        gkw = on.empty((D,), torch.float32) if want[3] else None
-        if workspace is None and (want[2] or want[3]):
-            n = qk_norm_rotary_backward_workspace_size(Hq, Hk, D)
-            workspace = on.empty(n, torch.uint8) if n else None
-        st = lib().kla_qk_norm_rotary_backward(
-            _ptr(q), qs, _ptr(k), ks, code, _ptr(q_weight), _ptr(k_weight), eps, freq, rot, int(interleaved), scale,
-            pos, batch, position0, _ptr(g_q), _ptr(g_k), _ptr(gq), _ptr(gk), _ptr(gqw), _ptr(gkw), B, T, Hq, Hk, D,
-            _ptr(workspace), workspace.numel() if workspace is not None else 0, on.handle)
-    _check(st, "kla_qk_norm_rotary_backward")
-    return gq, gk, gqw, gkw
+    index, sizes, args = _qk_call(q, k, q_weight, k_weight, eps, inv_freq, positions, position0, interleaved, scale)
+    pg = _need("g_q", g_q, q.shape, q.dtype, index), _need("g_k", g_k, k.shape, q.dtype, index)
+    pw, nw = _need_workspace(workspace, index)
+    want_q, want_k = want[0] and g_q is not None, want[1] and g_k is not None
+    want_qw = want[2] and g_q is not None and q_weight is not None
+    want_kw = want[3] and g_k is not None and k_weight is not None
+
+    def call(handle):
+        gq, gk = _empty_rows(q) if want_q else None, _empty_rows(k) if want_k else None
+        gqw, gkw = torch.empty_like(q_weight) if want_qw else None, torch.empty_like(k_weight) if want_kw else None
+        ws, n = pw, nw
+        if ws is None and (want_qw or want_kw):
+            n = qk_norm_rotary_backward_workspace_size(*sizes[2:])
+            room = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+            ws = _ptr(room)
+        _check(lib().kla_qk_norm_rotary_backward(*args, *pg, _ptr(gq), _ptr(gk), _ptr(gqw), _ptr(gkw), *sizes, ws, n,
+                                                 handle), "kla_qk_norm_rotary_backward")
+        return gq, gk, gqw, gkw
+
+    return _enqueue(index, stream, call)
 
 
 class QKNormRotary(torch.autograd.Function):

@@ -606,7 +606,7 @@ kla_gated_backward_kernel(const GatedBackwardParams prm) {
         const int nv = FULL ? L : (int)(tl + 1 < L ? tl + 1 : L);
         const unsigned char *const from = mine + (r & 1) * Stage::BYTES;
         const int64_t first = (row0 + g.T - 1 - s0) * hn + at.c0;
-        const int at_in = sub * In::PART + ch * VEC * (int)sizeof(Tin);
+        [[maybe_unused]] const int at_in = sub * In::PART + ch * VEC * (int)sizeof(Tin);
         const int at_wide = sub * Wide::PART + ch * VEC * 4;
         [[maybe_unused]] const float *const gate = gates + (HEAD && valid ? (c / g.N - head0) * R : 0) + sub * L;
         auto wide = [&](int part, int64_t row, int i) {

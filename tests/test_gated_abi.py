@@ -109,7 +109,7 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match=r"\[B, H, N\]"):
         kla.gated_scan_step(f, x, h0)
     with pytest.raises(ValueError, match="h_state"):
-        kla.gated_scan_step(f[:, 0], x[:, 0], h0[:, :2])
+        kla.gated_scan_step(f[:, 0].contiguous(), x[:, 0].contiguous(), h0[:, :2])
     with pytest.raises(TypeError, match="g_h"):
         kla.gated_scan_backward(f, x, x.bfloat16())
     with pytest.raises(ValueError, match="g_h"):
