@@ -25,21 +25,28 @@ bool sizes(int64_t B, int64_t T, int64_t H, int64_t N, kla_gate_t gate, Sizes *s
     return true;
 }
 
-// Tokens per warp and round.
+// Tokens of a lane in a round: as many as make 4 to 8 KB of a warp's rows in
+// flight (two channels a lane).  Forward, half as many: the long fp32 shape
+// (B=1, T=65536, 32 x 128) 580 us against 659 with 16 tokens; shared gates
+// 456 us with 16 against 508 with 8.  Backward: B=8, T=2048, 16 x 128 fp32 108 us
+// against 124 with 8; bf16 80 us with 8 against 85 with 4; shared gates, the
+// long fp32 shape, 822 us with 16 against 910 with 8.
 #ifndef KLA_GATED_L
-#define KLA_GATED_L 16
+#define KLA_GATED_L 0
 #endif
-#ifndef KLA_GATED_BACKWARD_L
-#define KLA_GATED_BACKWARD_L 8
-#endif
-// Clusters are doubled while the CTAs are fewer than this many per SM.
-#ifndef KLA_GATED_FILL
-#define KLA_GATED_FILL 2
-#endif
-// Tiles, in hundredths of the SMs, that are enough without narrower ones.
-#ifndef KLA_GATED_TILES
-#define KLA_GATED_TILES 100
-#endif
+template <typename Tin, bool HEAD, bool BACKWARD>
+constexpr int tokens_of_lane() {
+    if (KLA_GATED_L > 0) return KLA_GATED_L;
+    if (HEAD) return 16;
+    return BACKWARD && sizeof(Tin) == 4 ? 4 : 8;
+}
+int tokens_of_lane(kla_dtype_t dt, bool head, bool backward) {
+    if (dt == KLA_F32)
+        return head ? backward ? tokens_of_lane<float, true, true>() : tokens_of_lane<float, true, false>()
+                    : backward ? tokens_of_lane<float, false, true>() : tokens_of_lane<float, false, false>();
+    return head ? backward ? tokens_of_lane<__nv_bfloat16, true, true>() : tokens_of_lane<__nv_bfloat16, true, false>()
+                : backward ? tokens_of_lane<__nv_bfloat16, false, true>() : tokens_of_lane<__nv_bfloat16, false, false>();
+}
 
 struct Launch {
     GatedTiles g;
@@ -83,9 +90,13 @@ int copy_of(int64_t HN, int64_t seg, const Array *arrays, int n) {
     return start ? wide ? WIDE : SHIFT : NARROW;
 }
 
-// The widest tiles of which there are enough to fill the SMs: two channels a
-// lane (where rows start on such pairs and 16 bytes), one, or one and a warp's
-// lanes in 2 or 4 parts.  resident(vec, S, copy): warps that an SM holds.
+// The widest tiles of which there are enough: 0.8 of the SMs (shared gates,
+// the long fp32 shape: 128 tiles of 32 channels 424 us, 256 of 16 455; B=2, T=5001,
+// 12 x 80, 21 us against 27), or 1.5 of them with one channel a lane.  Rows that start
+// on 16 bytes, and on pairs of channels in every array, take two channels a
+// lane (half the instructions for a channel, and two chains of multiply-adds
+// side by side), others one; a warp's lanes in 1, 2, 4 or 8 parts.
+// resident(vec, S, copy): warps that an SM holds.
 template <typename F>
 Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, bool head, int L, const Array *arrays, int n, F resident) {
     Launch l;
@@ -93,26 +104,39 @@ Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, bool head, int L, const 
     l.g.T = T; l.g.H = H; l.g.N = N; l.g.HN = HN;
     bool pairs = HN % 2 == 0 && (!head || N % 2 == 0);
     for (int i = 0; i < n; ++i) pairs = pairs && aligned(arrays[i].p, 2 * arrays[i].size);
-    constexpr int kForms[4][2] = {{2, 1}, {1, 1}, {1, 2}, {1, 4}};
+    constexpr int kForms[7][2] = {{2, 1}, {2, 2}, {2, 4}, {2, 8}, {1, 1}, {1, 2}, {1, 4}};
+    bool any = false;
     for (const auto &form : kForms) {
         const int vec = form[0], S = form[1];
-        if (vec == 2 && !pairs) continue;
         Launch k = l;
         tile(B, H, N, head, vec, S, &k);
         k.copy = copy_of(HN, k.g.seg, arrays, n);
-        if (vec == 2 && k.copy != WIDE) continue;
-        if (S > 1 && (k.copy == NARROW || (T + L - 1) / L < S)) break;
+        if (vec == 2 ? !pairs || k.copy != WIDE : any) continue;
+        if (vec == 1 && k.copy == WIDE) k.copy = SHIFT;
+        // parts no shorter than a sector of memory a row
+        if (S > 1 && (k.copy == NARROW || (T + L - 1) / L < S || (vec == 2 && 64 / S * arrays[0].size < 32)))
+            continue;
         l = k;
-        if (l.tiles * 100 >= sms * KLA_GATED_TILES) break;
+        any = any || vec == 2;
+        if (vec == 2 ? 5 * l.tiles >= 4 * sms : 2 * l.tiles >= 3 * sms) break;
     }
     const int64_t chunks = (T + l.S * L - 1) / (l.S * L);  // of a warp
-    // few tiles all the same: clusters, until the CTAs are KLA_GATED_FILL for each SM
+    const int64_t held = resident(l.vec, l.S, l.copy);
     l.C = 1;
-    l.W = (int)std::min<int64_t>(kGatedMaxWarps, chunks);
-    while (l.C < kGatedMaxCluster && 2 * l.tiles * l.C <= KLA_GATED_FILL * sms && (int64_t)l.C * l.W < chunks) l.C *= 2;
+    l.W = (int)std::min({(int64_t)8, held, chunks});
+    if (3 * l.tiles <= 2 * sms) {
+        // few tiles all the same: clusters, until there are two CTAs for each SM
+        while (l.C < kGatedMaxCluster && l.tiles * l.C <= sms && (int64_t)l.C * l.W < chunks) l.C *= 2;
+    } else if (l.tiles <= sms && chunks >= 32 * kGatedMaxWarps) {
+        // one CTA an SM, and a long sequence: as many warps as have 64 KB of
+        // rows in a round (the long fp32 shape: 515 us with 16 against 608
+        // with 8; backward 922 against 1132)
+        l.W = (int)std::max<int64_t>(
+            l.W, std::min({(int64_t)kGatedMaxWarps, held, 64 * 1024 / resident.stage(l.vec, l.S, l.copy)}));
+    }
     // many tiles: fewer warps each, so that all are resident at once (CTAs
     // that had to wait for others would run alone at the end)
-    while (l.C == 1 && l.W > 1 && l.tiles * l.W > resident(l.vec, l.S, l.copy) * sms) l.W = (l.W + 1) / 2;
+    if (l.C == 1) l.W = (int)std::max<int64_t>(1, std::min<int64_t>(l.W, held / ((l.tiles + sms - 1) / sms)));
     return l;
 }
 
@@ -160,19 +184,20 @@ constexpr int smem_bytes(int stage, int W, int C) {
 
 template <auto KERNEL, int VEC, typename Params>
 cudaError_t run(const Launch &l, int stage, const Params &prm, cudaStream_t st) {
-    const cudaError_t e = allow_smem<KERNEL>(smem_bytes<VEC>(stage, kGatedMaxWarps, kGatedMaxCluster));
+    const cudaError_t e = allow_smem<KERNEL>(
+        std::min(227 * 1024, smem_bytes<VEC>(stage, kGatedMaxWarps, kGatedMaxCluster)));
     if (e != cudaSuccess) return e;
     return launch(KERNEL, l.tiles * l.C, 32 * l.W, l.C, (size_t)smem_bytes<VEC>(stage, l.W, l.C), st, prm);
 }
 
 template <typename Tin, int VEC, int S, bool HEAD, int COPY>
 cudaError_t run_scan(const Launch &l, const GatedParams &prm, cudaStream_t st) {
-    constexpr int L = KLA_GATED_L, STAGE = GatedStage<Tin, VEC, S, HEAD, L, COPY, false>::WARP;
+    constexpr int L = tokens_of_lane<Tin, HEAD, false>(), STAGE = GatedStage<Tin, VEC, S, HEAD, L, COPY, false>::WARP;
     return run<kla_gated_forward_kernel<Tin, VEC, S, HEAD, L, COPY>, VEC>(l, STAGE, prm, st);
 }
 template <typename Tin, int VEC, int S, bool HEAD, int COPY>
 cudaError_t run_scan(const Launch &l, const GatedBackwardParams &prm, cudaStream_t st) {
-    constexpr int L = KLA_GATED_BACKWARD_L, STAGE = GatedStage<Tin, VEC, S, HEAD, L, COPY, true>::WARP;
+    constexpr int L = tokens_of_lane<Tin, HEAD, true>(), STAGE = GatedStage<Tin, VEC, S, HEAD, L, COPY, true>::WARP;
     return run<kla_gated_backward_kernel<Tin, VEC, S, HEAD, L, COPY>, VEC>(l, STAGE, prm, st);
 }
 // The forms that plan() chooses from.
@@ -183,10 +208,10 @@ cudaError_t run_form(const Launch &l, const Params &prm, cudaStream_t st) {
         return l.S == 1   ? run_scan<Tin, 1, 1, HEAD, SHIFT>(l, prm, st)
                : l.S == 2 ? run_scan<Tin, 1, 2, HEAD, SHIFT>(l, prm, st)
                           : run_scan<Tin, 1, 4, HEAD, SHIFT>(l, prm, st);
-    if (l.vec == 2) return run_scan<Tin, 2, 1, HEAD, WIDE>(l, prm, st);
-    return l.S == 1   ? run_scan<Tin, 1, 1, HEAD, WIDE>(l, prm, st)
-           : l.S == 2 ? run_scan<Tin, 1, 2, HEAD, WIDE>(l, prm, st)
-                      : run_scan<Tin, 1, 4, HEAD, WIDE>(l, prm, st);
+    return l.S == 1   ? run_scan<Tin, 2, 1, HEAD, WIDE>(l, prm, st)
+           : l.S == 2 ? run_scan<Tin, 2, 2, HEAD, WIDE>(l, prm, st)
+           : l.S == 4 ? run_scan<Tin, 2, 4, HEAD, WIDE>(l, prm, st)
+                      : run_scan<Tin, 2, 8, HEAD, WIDE>(l, prm, st);
 }
 template <typename Params>
 cudaError_t run_type(const Launch &l, kla_dtype_t dt, bool head, const Params &prm, cudaStream_t st) {
@@ -197,15 +222,19 @@ cudaError_t run_type(const Launch &l, kla_dtype_t dt, bool head, const Params &p
 // Warps that an SM holds at once, by registers and by shared memory (two
 // rounds of rows a warp, as GatedStage has them).
 struct Resident {
-    int64_t e;
+    int64_t e, L;
     bool head, backward;
-    int64_t operator()(int vec, int S, int copy) const {
-        const int64_t L = backward ? KLA_GATED_BACKWARD_L : KLA_GATED_L;
+    // bytes of a warp's rows in one round
+    int64_t stage(int vec, int S, int copy) const {
         const int64_t pad = copy == SHIFT ? 16 : 0, cw = 32 / S * vec, apart = S > 1 ? cw : 0;
-        const int64_t wide = 2 * S * (L * (4 * cw + pad) + 4 * apart), in = 2 * S * (L * (e * cw + pad) + e * apart);
-        const int64_t bytes = (backward ? 2 * wide : in) + (head ? L * kGatedHeads * 4 : in) + 512 * vec;
-        return std::min<int64_t>(kGatedMaxWarps * (backward ? KLA_GATED_BACKWARD_MINB : KLA_GATED_MINB),
-                                 224 * 1024 / bytes);
+        const int64_t wide = S * (L * (4 * cw + pad) + 4 * apart), in = S * (L * (e * cw + pad) + e * apart);
+        return (backward ? 2 * wide : in) + (head ? 0 : in);
+    }
+    int64_t operator()(int vec, int S, int copy) const {
+        const int64_t rounds = e == 2 && !head && !backward ? 3 : 2;
+        const int64_t bytes = rounds * stage(vec, S, copy) + (head ? L * kGatedHeads * 4 : 0) + 512 * vec;
+        return std::min<int64_t>(65536 / (32 * (backward ? KLA_GATED_BACKWARD_REGS : KLA_GATED_REGS)) / 4 * 4,
+                                 226 * 1024 / bytes);
     }
 };
 
@@ -256,7 +285,8 @@ KLA_API kla_status_t kla_gated_scan_forward(const void *f, const void *x, kla_dt
     // a gate for each head of one channel is a gate for each channel
     const bool head = gate == KLA_GATE_HEAD && N > 1;
     const Array arrays[3] = {{x, e, true}, {h, 4, false}, {f, e, true}};
-    const Launch l = plan(B, T, H, N, head, KLA_GATED_L, arrays, head ? 2 : 3, Resident{e, head, false});
+    const int L = tokens_of_lane(in_dtype, head, false);
+    const Launch l = plan(B, T, H, N, head, L, arrays, head ? 2 : 3, Resident{e, L, head, false});
     if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
     GatedParams prm;
     prm.g = l.g;
@@ -332,7 +362,8 @@ KLA_API kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype
     const bool head = gate == KLA_GATE_HEAD && N > 1;
     const Array arrays[5] = {{g_h, 4, true}, {grad_f ? h : nullptr, 4, true}, {grad_x, e, false},
                              {f, e, true}, {grad_f, e, false}};
-    const Launch l = plan(B, T, H, N, head, KLA_GATED_BACKWARD_L, arrays, head ? 3 : 5, Resident{e, head, true});
+    const int L = tokens_of_lane(in_dtype, head, true);
+    const Launch l = plan(B, T, H, N, head, L, arrays, head ? 3 : 5, Resident{e, L, head, true});
     if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
     const int64_t parts = head ? parts_of(N, 32 / l.S * l.vec) : 1;
     GatedBackwardParams prm;

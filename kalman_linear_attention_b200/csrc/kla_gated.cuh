@@ -49,13 +49,23 @@
 
 namespace kla_mixer {
 
-constexpr int kGatedMaxWarps = 8;
-// CTAs per SM that the kernels' registers leave room for.
-#ifndef KLA_GATED_MINB
-#define KLA_GATED_MINB 3
+#ifndef KLA_GATED_WARPS
+#define KLA_GATED_WARPS 16
 #endif
-#ifndef KLA_GATED_BACKWARD_MINB
-#define KLA_GATED_BACKWARD_MINB 2
+constexpr int kGatedMaxWarps = KLA_GATED_WARPS;
+// Rounds of rows that a warp holds: the present one, and one asked for; or two
+// asked for, of fewer tokens, forward with a bf16 gate for each channel (B=8,
+// T=2048, 16 x 128: 49 us against 52; fp32 took 76 us against 66 so).
+template <typename Tin, bool HEAD, bool BACKWARD>
+__host__ __device__ constexpr int gated_rounds() {
+    return sizeof(Tin) == 2 && !HEAD && !BACKWARD ? 3 : 2;
+}
+// Registers of a thread, forward and backward: 24 and 16 warps on an SM.
+#ifndef KLA_GATED_REGS
+#define KLA_GATED_REGS 80
+#endif
+#ifndef KLA_GATED_BACKWARD_REGS
+#define KLA_GATED_BACKWARD_REGS 120
 #endif
 constexpr int kGatedMaxCluster = 8;
 
@@ -313,21 +323,29 @@ struct Rows {
 // Gates shared by heads: those of a warp's R = S L tokens and up to kGatedHeads
 // / S heads of the tile, a few in each lane, one round ahead.
 constexpr int kGatedHeads = 8;
-template <typename Tin, int S, int L>
+template <typename Tin, int S, int L, int ROUNDS>
 struct HeadGates {
     static constexpr int R = S * L;
     static constexpr int N = L * kGatedHeads / 32;
-    Tin ahead[N];
+    Tin ahead[ROUNDS - 1][N];
 
+    // Make room for the next round's.
+    __device__ __forceinline__ void shift() {
+#pragma unroll
+        for (int k = 0; k + 1 < ROUNDS - 1; ++k)
+#pragma unroll
+            for (int n = 0; n < N; ++n) ahead[k][n] = ahead[k + 1][n];
+    }
     // Token i of head k: at from + i * step + k, where lo <= i < hi.
     __device__ __forceinline__ void ask(const Tin *from, int64_t step, int heads, int lo, int hi) {
         const int lane = threadIdx.x & 31;
+        Tin(&last)[N] = ahead[ROUNDS - 2];
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int i = (n * 32 + lane) % R, k = (n * 32 + lane) / R;
             if (n * 32 < heads * R) {  // uniform
-                ahead[n] = from_float<Tin>(1.f);
-                if (k < heads && i >= lo && i < hi) ahead[n] = from[i * step + k];
+                last[n] = from_float<Tin>(1.f);
+                if (k < heads && i >= lo && i < hi) last[n] = from[i * step + k];
             }
         }
     }
@@ -336,11 +354,11 @@ struct HeadGates {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            if (n * 32 + lane < heads * R) to[n * 32 + lane] = to_float(ahead[n]);
+            if (n * 32 + lane < heads * R) to[n * 32 + lane] = to_float(ahead[0][n]);
     }
 };
 
-// Shared memory of a warp, in bytes: two rounds of its rows, and the gates
+// Shared memory of a warp, in bytes: its rounds of rows, and the gates
 // shared by heads.
 template <typename Tin, int VEC, int S, bool HEAD, int L, int COPY, bool BACKWARD>
 struct GatedStage {
@@ -351,7 +369,8 @@ struct GatedStage {
     static constexpr int H = X + (BACKWARD ? Wide::BYTES : In::BYTES);  // rows of h
     static constexpr int F = H + (BACKWARD ? Wide::BYTES : 0);          // rows of f
     static constexpr int BYTES = F + (HEAD ? 0 : In::BYTES);
-    static constexpr int GATES = 2 * BYTES;
+    static constexpr int ROUNDS = gated_rounds<Tin, HEAD, BACKWARD>();
+    static constexpr int GATES = ROUNDS * BYTES;
     static constexpr int WARP = GATES + (HEAD ? L * kGatedHeads * 4 : 0);
     static_assert(BYTES % 16 == 0 && WARP % 16 == 0, "16-byte pieces");
 };
@@ -359,7 +378,8 @@ struct GatedStage {
 // Grid: tiles x C CTAs of 32 x W threads.  Dynamic shared memory: GatedStage of
 // each warp, then the pairs.
 template <typename Tin, int VEC, int S, bool HEAD, int L, int COPY>
-__global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_MINB) kla_gated_forward_kernel(const GatedParams prm) {
+__global__ void __maxnreg__(KLA_GATED_REGS)
+kla_gated_forward_kernel(const GatedParams prm) {
     using Stage = GatedStage<Tin, VEC, S, HEAD, L, COPY, false>;
     using In = typename Stage::In;
     using Pairs = typename GatedPairs<VEC>::Pairs;
@@ -380,7 +400,7 @@ __global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_MINB) kla_gated
     const int heads = HEAD ? (int)((at.c0 + width - 1) / g.N - head0) + 1 : 0;
     const Tin *const f = static_cast<const Tin *>(prm.f);
     const Tin *const x = static_cast<const Tin *>(prm.x);
-    float *const h = prm.h + row0 * g.HN + c;
+    float *const h = prm.h + ch * VEC;
     unsigned char *const mine = shared + w * Stage::WARP;
     float *const gates = reinterpret_cast<float *>(mine + Stage::GATES);
     Pairs *const pairs = reinterpret_cast<Pairs *>(shared + W * Stage::WARP);
@@ -390,34 +410,36 @@ __global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_MINB) kla_gated
 #pragma unroll
     for (int v = 0; v < VEC; ++v) carry[v] = prm.h0 && valid ? prm.h0[at.b * g.HN + c + v] : 0.f;
 
-    const int64_t span = (int64_t)W * R;
-    const int64_t rounds = (g.T + span * C - 1) / (span * C);
-    HeadGates<Tin, S, L> ahead;
-    auto ask_rows = [&](auto full, int64_t r) {
+    // where this warp is in a round: the first element of its rows, their
+    // gates, and the tokens from there to the end (none when not positive)
+    const int64_t t0 = (int64_t)(rank * W + w) * R, round = (int64_t)C * W * R;
+    const int64_t rounds = (g.T + round - 1) / round;
+    const bool whole = width == Stage::CW;
+    HeadGates<Tin, S, L, Stage::ROUNDS> ahead;
+    auto ask_rows = [&](auto full, int buf, int64_t first, const Tin *gate_rows, int64_t left) {
         constexpr bool FULL = decltype(full)::value;
-        const int64_t hn = opaque(g.HN), t0 = (r * C + rank) * span + w * R;
-        const int nv = FULL ? R : (int)(g.T - t0 < R ? g.T - t0 : R);
-        unsigned char *const to = mine + (r & 1) * Stage::BYTES;
-        const int64_t first = (row0 + t0) * hn + at.c0;
+        const int64_t hn = opaque(g.HN);
+        const int nv = FULL ? R : (int)(left < R ? left : R);
+        unsigned char *const to = mine + buf * Stage::BYTES;
         In::template ask<FULL>(to + Stage::X, x, prm.n, first, hn, 0, nv, width);
         if constexpr (HEAD)
-            ahead.ask(f + (row0 + t0) * g.H + head0, g.H, heads, 0, nv);
+            ahead.ask(gate_rows, g.H, heads, 0, nv);
         else
             In::template ask<FULL>(to + Stage::F, f, prm.n, first, hn, 0, nv, width);
         copies_commit();
     };
     // FULL rounds of a warp, all of whose tokens and channels are there, take
     // code without their tests (a third of the instructions)
-    auto full = [&](int64_t r) { return (r * C + rank) * span + w * R + R <= g.T && width == Stage::CW; };
-    auto ask = [&](int64_t r) { full(r) ? ask_rows(Yes{}, r) : ask_rows(No{}, r); };
-    auto run = [&](auto full_, int64_t r) {
+    auto ask = [&](int buf, int64_t first, const Tin *gate_rows, int64_t left) {
+        whole && left >= R ? ask_rows(Yes{}, buf, first, gate_rows, left) : ask_rows(No{}, buf, first, gate_rows, left);
+    };
+    auto run = [&](auto full_, int buf, int parity, int64_t first, int64_t left_of_warp) {
         constexpr bool FULL = decltype(full_)::value;
-        const int64_t hn = opaque(g.HN), t0 = (r * C + rank) * span + w * R;
-        const int64_t left = g.T - t0 - sub * L;  // of this lane's tokens
+        const int64_t hn = opaque(g.HN);
+        const int64_t left = left_of_warp - sub * L;  // of this lane's tokens
         const int nv = FULL ? L : (int)(left < L ? left : L);
-        const unsigned char *const from = mine + (r & 1) * Stage::BYTES;
+        const unsigned char *const from = mine + buf * Stage::BYTES;
         // tokens that are not there leave the state as it is: f = 1, x = 0
-        const int64_t first = (row0 + t0) * hn + at.c0;
         const int at_lane = sub * In::PART + ch * VEC * (int)sizeof(Tin);
         [[maybe_unused]] const float *const gate = gates + (HEAD && valid ? (c / g.N - head0) * R : 0) + sub * L;
         auto pack = [&](int part, int i) {
@@ -451,8 +473,8 @@ __global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_MINB) kla_gated
                 z[v] = fmaf(fi[v], z[v], to_float(xi.v[v]));
             }
         }
-        exchange<VEC, S>(sh, (int)(r & 1), w, W, rank, C, A, z, carry, entry);
-        float *ht = h + (t0 + sub * L) * hn;
+        exchange<VEC, S>(sh, parity, w, W, rank, C, A, z, carry, entry);
+        float *ht = h + first + sub * L * hn;
 #pragma unroll
         for (int i = 0; i < L; ++i, ht += hn) {
             const Pack<Tin, VEC> xi = x_at(i);
@@ -467,20 +489,39 @@ __global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_MINB) kla_gated
         }
     };
 
-    ask(0);
-    if (C > 1) cluster_barrier();  // every rank runs before its shared memory is written
-#pragma unroll 1
-    for (int64_t r = 0; r < rounds; ++r) {
-        __syncwarp();  // the other stage and the gates have been read
-        if (HEAD) ahead.give(gates, heads);
-        if (r + 1 < rounds) {
-            ask(r + 1);
-            copies_wait<1>();
+    int64_t first = (row0 + t0) * g.HN + at.c0, left = g.T - t0;
+    int64_t first_asked = first, left_asked = left;
+    const Tin *gate_rows = HEAD ? f + (row0 + t0) * g.H + head0 : nullptr;
+    const int64_t first_step = round * g.HN, gate_step = HEAD ? round * g.H : 0;
+    // the rounds asked for are `asked` ahead of the present one
+    int64_t asked = 0;
+    int to_buf = 0;
+    auto ask_next = [&]() {
+        if (HEAD) ahead.shift();
+        if (asked < rounds) {
+            ask(to_buf, first_asked, gate_rows, left_asked);
+            first_asked += first_step;
+            gate_rows += gate_step;
+            left_asked -= round;
         } else {
-            copies_wait<0>();
+            copies_commit();
         }
+        ++asked;
+        to_buf = to_buf == Stage::ROUNDS - 1 ? 0 : to_buf + 1;
+    };
+#pragma unroll
+    for (int k = 0; k < Stage::ROUNDS - 1; ++k) ask_next();
+    if (C > 1) cluster_barrier();  // every rank runs before its shared memory is written
+    int buf = 0;
+#pragma unroll 1
+    for (int64_t r = 0; r < rounds; ++r, first += first_step, left -= round) {
+        __syncwarp();  // the stage to fill and the gates have been read
+        if (HEAD) ahead.give(gates, heads);
+        ask_next();
+        copies_wait<Stage::ROUNDS - 1>();
         __syncwarp();
-        full(r) ? run(Yes{}, r) : run(No{}, r);
+        whole && left >= R ? run(Yes{}, buf, (int)(r & 1), first, left) : run(No{}, buf, (int)(r & 1), first, left);
+        buf = buf == Stage::ROUNDS - 1 ? 0 : buf + 1;
     }
 }
 
@@ -537,7 +578,7 @@ struct GroupSums {
 // Grid: tiles x C CTAs of 32 x W threads; token s of the kernel is T-1-s.
 // Dynamic shared memory as in the forward kernel.
 template <typename Tin, int VEC, int S, bool HEAD, int L, int COPY>
-__global__ void __launch_bounds__(32 * kGatedMaxWarps, KLA_GATED_BACKWARD_MINB)
+__global__ void __maxnreg__(KLA_GATED_BACKWARD_REGS)
 kla_gated_backward_kernel(const GatedBackwardParams prm) {
     using Stage = GatedStage<Tin, VEC, S, HEAD, L, COPY, true>;
     using In = typename Stage::In;
@@ -572,40 +613,40 @@ kla_gated_backward_kernel(const GatedBackwardParams prm) {
 #pragma unroll
     for (int v = 0; v < VEC; ++v) carry[v] = 0.f;
 
-    const int64_t span = (int64_t)W * R;
-    const int64_t rounds = (g.T + span * C - 1) / (span * C);
-    HeadGates<Tin, S, L> ahead;
+    // as in the forward kernel, in reverse time: the first of a warp's rows is
+    // its last token's, and `left` counts the tokens from there down to the first
+    const int64_t t0 = (int64_t)(rank * W + w) * R, round = (int64_t)C * W * R;
+    const int64_t rounds = (g.T + round - 1) / round;
+    const bool whole = width == Stage::CW;
+    HeadGates<Tin, S, L, Stage::ROUNDS> ahead;
     // of token t: g; h of token t - 1 (none before the first); f of token t + 1
     // (none after the last)
-    auto ask_rows = [&](auto full, int64_t r) {
+    auto ask_rows = [&](auto full, int buf, int64_t first, const Tin *gate_rows, int64_t left) {
         constexpr bool FULL = decltype(full)::value;
-        const int64_t hn = opaque(g.HN), s0 = (r * C + rank) * span + w * R;
-        const int nv = FULL ? R : (int)(g.T - s0 < R ? g.T - s0 : R);
-        const int64_t tl = g.T - 1 - s0;  // the chunk's last token; it walks down
-        unsigned char *const to = mine + (r & 1) * Stage::BYTES;
-        const int64_t first = (row0 + tl) * hn + at.c0;
+        const int64_t hn = opaque(g.HN);
+        const int nv = FULL ? R : (int)(left < R ? left : R);
+        const int lo = FULL || left < g.T ? 0 : 1, before = FULL ? R : (int)(left - 1 < R ? left - 1 : R);
+        unsigned char *const to = mine + buf * Stage::BYTES;
         Wide::template ask<FULL>(to + Stage::X, prm.gh, prm.n, first, -hn, 0, nv, width);
-        if (h)
-            Wide::template ask<FULL>(to + Stage::H, h, prm.n, first - hn, -hn, 0, tl < nv ? (int)tl : nv, width);
+        if (h) Wide::template ask<FULL>(to + Stage::H, h, prm.n, first - hn, -hn, 0, before, width);
         if constexpr (HEAD)
-            ahead.ask(f + (row0 + tl + 1) * g.H + head0, -g.H, heads, s0 > 0 ? 0 : 1, nv);
+            ahead.ask(gate_rows, -g.H, heads, lo, nv);
         else
-            In::template ask<FULL>(to + Stage::F, f, prm.n, first + hn, -hn, s0 > 0 ? 0 : 1, nv, width);
+            In::template ask<FULL>(to + Stage::F, f, prm.n, first + hn, -hn, lo, nv, width);
         copies_commit();
     };
     // FULL: as in the forward kernel, with the tokens before and after
-    auto full = [&](int64_t r) {
-        const int64_t s0 = (r * C + rank) * span + w * R;
-        return s0 > 0 && s0 + R < g.T && width == Stage::CW;
+    auto is_full = [&](int64_t left) { return whole && left < g.T && left > R; };
+    auto ask = [&](int buf, int64_t first, const Tin *gate_rows, int64_t left) {
+        is_full(left) ? ask_rows(Yes{}, buf, first, gate_rows, left) : ask_rows(No{}, buf, first, gate_rows, left);
     };
-    auto ask = [&](int64_t r) { full(r) ? ask_rows(Yes{}, r) : ask_rows(No{}, r); };
-    auto run = [&](auto full_, int64_t r) {
+    auto run = [&](auto full_, int buf, int parity, int64_t first, int64_t left_of_warp) {
         constexpr bool FULL = decltype(full_)::value;
-        const int64_t hn = opaque(g.HN), s0 = (r * C + rank) * span + w * R;
-        const int64_t tl = g.T - 1 - s0 - sub * L;  // this lane's last token
+        const int64_t hn = opaque(g.HN);
+        const int64_t tl = left_of_warp - 1 - sub * L;  // this lane's last token
         const int nv = FULL ? L : (int)(tl + 1 < L ? tl + 1 : L);
-        const unsigned char *const from = mine + (r & 1) * Stage::BYTES;
-        const int64_t first = (row0 + g.T - 1 - s0) * hn + at.c0;
+        [[maybe_unused]] const bool at_end = !FULL && left_of_warp == g.T && sub == 0;  // its last token is the sequence's
+        const unsigned char *const from = mine + buf * Stage::BYTES;
         [[maybe_unused]] const int at_in = sub * In::PART + ch * VEC * (int)sizeof(Tin);
         const int at_wide = sub * Wide::PART + ch * VEC * 4;
         [[maybe_unused]] const float *const gate = gates + (HEAD && valid ? (c / g.N - head0) * R : 0) + sub * L;
@@ -620,7 +661,7 @@ kla_gated_backward_kernel(const GatedBackwardParams prm) {
                 for (int v = 0; v < VEC; ++v) to[v] = pack_at<float, 4>(gate + i / 4 * 4).v[i % 4];
             } else {
                 Pack<Tin, VEC> p = pack_of<Tin, VEC>(1.f);
-                if (FULL || (i < nv && s0 + sub * L + i > 0))
+                if (FULL || (i < nv && !(at_end && i == 0)))
                     p = pack_at<Tin, VEC>(reinterpret_cast<const Tin *>(from + Stage::F + at_in + i * In::PITCH +
                                                                         In::shift(first + hn, -hn, sub * L + i)));
 #pragma unroll
@@ -643,9 +684,9 @@ kla_gated_backward_kernel(const GatedBackwardParams prm) {
                 z[v] = fmaf(fi[v], z[v], gi.v[v]);
             }
         }
-        exchange<VEC, S>(sh, (int)(r & 1), w, W, rank, C, A, z, carry, entry);
+        exchange<VEC, S>(sh, parity, w, W, rank, C, A, z, carry, entry);
         GroupSums<L> sum;  // HEAD: this lane's share of the shared gate's gradient
-        const int64_t out = (row0 + tl) * hn + c;
+        const int64_t out = first - sub * L * hn + ch * VEC;
         Tin *gxt = gx + out;
         Tin *gft = gf + out;
 #pragma unroll
@@ -705,20 +746,39 @@ kla_gated_backward_kernel(const GatedBackwardParams prm) {
         }
     };
 
-    ask(0);
-    if (C > 1) cluster_barrier();
-#pragma unroll 1
-    for (int64_t r = 0; r < rounds; ++r) {
-        __syncwarp();  // the other stage and the gates have been read
-        if (HEAD) ahead.give(gates, heads);
-        if (r + 1 < rounds) {
-            ask(r + 1);
-            copies_wait<1>();
+    int64_t first = (row0 + g.T - 1 - t0) * g.HN + at.c0, left = g.T - t0;
+    int64_t first_asked = first, left_asked = left;
+    const Tin *gate_rows = HEAD ? f + (row0 + g.T - t0) * g.H + head0 : nullptr;
+    const int64_t first_step = -round * g.HN, gate_step = HEAD ? -round * g.H : 0;
+    // the rounds asked for are `asked` ahead of the present one
+    int64_t asked = 0;
+    int to_buf = 0;
+    auto ask_next = [&]() {
+        if (HEAD) ahead.shift();
+        if (asked < rounds) {
+            ask(to_buf, first_asked, gate_rows, left_asked);
+            first_asked += first_step;
+            gate_rows += gate_step;
+            left_asked -= round;
         } else {
-            copies_wait<0>();
+            copies_commit();
         }
+        ++asked;
+        to_buf = to_buf == Stage::ROUNDS - 1 ? 0 : to_buf + 1;
+    };
+#pragma unroll
+    for (int k = 0; k < Stage::ROUNDS - 1; ++k) ask_next();
+    if (C > 1) cluster_barrier();
+    int buf = 0;
+#pragma unroll 1
+    for (int64_t r = 0; r < rounds; ++r, first += first_step, left -= round) {
+        __syncwarp();  // the stage to fill and the gates have been read
+        if (HEAD) ahead.give(gates, heads);
+        ask_next();
+        copies_wait<Stage::ROUNDS - 1>();
         __syncwarp();
-        full(r) ? run(Yes{}, r) : run(No{}, r);
+        is_full(left) ? run(Yes{}, buf, (int)(r & 1), first, left) : run(No{}, buf, (int)(r & 1), first, left);
+        buf = buf == Stage::ROUNDS - 1 ? 0 : buf + 1;
     }
 }
 
