@@ -17,6 +17,10 @@ using namespace kla_mixer;
 #define KLA_ROTARY_ROWS 8
 #endif
 
+#ifndef KLA_ROTARY_ITEMS
+#define KLA_ROTARY_ITEMS 2
+#endif
+
 // What one call works on, checked: everything but the tensors.
 struct Call {
     RotaryParams prm = {};
@@ -125,7 +129,7 @@ void choose_items(Call *c, int tensors, bool backward) {
         // heads that a warp takes at once: few, so that a group has many heads
         // and cos and sin serve them all; more where warps would be idle
         int64_t n = 1;
-        while (n < abreast && n < h && (n * KLA_ROTARY_ROWS < h || c->prm.tokens * n < fill * abreast)) n *= 2;
+        while (n < abreast && n < h && (n * KLA_ROTARY_ROWS < h || c->prm.tokens * n < KLA_ROTARY_ITEMS * fill * abreast)) n *= 2;
         t.abreast = (int)n;
         const int64_t shares = (c->prm.tokens + abreast / n - 1) / (abreast / n);
         const int64_t most = (h + n - 1) / n;  // one head a group
