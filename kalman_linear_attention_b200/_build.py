@@ -1,9 +1,11 @@
-"""Compile the CUDA library ``libkla.so`` in-tree for sm_100a with nvcc."""
+"""Compile the CUDA library ``libkla.so`` in-tree for sm_100a with nvcc, and the
+CPython extension ``_mixer.so`` that binds the mixer operators."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -11,7 +13,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libkla.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("kla.cu", "kla_host.cu", "kla_gated.cu", "kla_rotary.cu")]
-DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "kla.h")]
+BINDING = os.path.join(HERE, "_mixer.so")
+BINDING_SOURCE = os.path.join(CSRC, "kla_binding.cpp")
+DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "kla_binding.cpp"] + [os.path.join(INCLUDE, "kla.h")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",
@@ -37,7 +41,14 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build libkla.so next to this file (no-op when it is newer than its sources)."""
+    """Build libkla.so and _mixer.so next to this file (each a no-op when it is
+    newer than its sources)."""
+    build_library(force, verbose)
+    build_binding(force)
+    return LIBRARY
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIBRARY
     tmp = LIBRARY + ".tmp"
@@ -47,6 +58,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIBRARY)
     return LIBRARY
+
+
+def build_binding(force: bool = False) -> str:
+    """_mixer.so, linked to torch's libraries and to libkla.so beside it."""
+    depends = [BINDING_SOURCE, os.path.join(INCLUDE, "kla.h")]
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in depends):
+        return BINDING
+    import torch
+    from torch.utils import cpp_extension
+    tmp = BINDING + ".tmp"
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    includes = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_paths()["include"], cuda]
+    libraries = [p for p in cpp_extension.library_paths() if os.path.isdir(p)]
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", BINDING_SOURCE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-isystem{p}" for p in includes], "-o", tmp, *[f"-L{p}" for p in libraries], f"-L{HERE}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-l:libkla.so", "-Wl,-rpath,$ORIGIN"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

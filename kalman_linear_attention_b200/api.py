@@ -1,4 +1,5 @@
-"""Thin Python binding of the C ABI in ``include/kla.h`` (ctypes).
+"""Thin Python binding of the C ABI in ``include/kla.h`` (ctypes; the mixer
+operators through the CPython extension ``_mixer``).
 
 Argument marshalling only: every step of the filter runs in the CUDA kernels
 of ``libkla.so``.  PyTorch is used for device memory and streams.  There is no
@@ -657,75 +658,25 @@ def scan_forward_lti(a: torch.Tensor, phi: torch.Tensor, b: torch.Tensor, lam0: 
 
 
 # ------------------------------------------------ gated linear recurrence
-# The current stream of a device as a plain handle: constructing a
-# torch.cuda.Stream for it takes longer than the rest of a call.
-_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_CODES = {torch.float32: KLA_F32, torch.bfloat16: KLA_BF16}
+# The mixer operators are bound natively (csrc/kla_binding.cpp): their checks,
+# allocations and stream take about as long there as one of these calls takes
+# the GPU.
+_mixer = None
 
 
-def _enqueue(index: int, stream: Optional[torch.cuda.Stream], call):
-    """``call(handle)`` with device ``index`` current and its work on
-    ``stream`` (default: the device's current stream), so that what the call
-    allocates belongs to that stream, whichever one is current outside."""
-    if index < 0:
-        raise ValueError("tensors must be on a CUDA device")
-    if stream is None:
-        if index == torch.cuda.current_device():
-            return call(_current_handle(index))
-        with torch.cuda.device(index):
-            return call(_current_handle(index))
-    if stream.device.index != index:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
-    with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
-
-
-def _refuse(name: str, t: torch.Tensor, shape, dtype: torch.dtype, index: int):
-    """Why a tensor that should be dense, of this shape and type and on this
-    device is not accepted."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on the device of the other tensors; it is on {t.device}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _need(name: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, index: int) -> Optional[int]:
-    """The address of a dense tensor of this shape and type on device `index`
-    (None: of no tensor)."""
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
-        _refuse(name, t, shape, dtype, index)
-    return t.data_ptr()
-
-
-def _need_workspace(t: Optional[torch.Tensor], index: int) -> Tuple[Optional[int], int]:
-    if t is None:
-        return None, 0
-    return _need("workspace", t, t.shape, t.dtype, index), t.numel() * t.element_size()
-
-
-def _gate(f: torch.Tensor, shape) -> int:
-    """The gate layout of f for states of `shape` ([.., H, N])."""
-    if f.shape == shape:
-        return KLA_GATE_CHANNEL
-    if f.shape == shape[:-1]:
-        return KLA_GATE_HEAD
-    raise ValueError(f"f must be {list(shape)} (a gate per channel) or {list(shape[:-1])} (shared by a head), "
-                     f"got {list(f.shape)}")
-
-
-def _gates_and_inputs(f: torch.Tensor, x: torch.Tensor) -> Tuple[int, int]:
-    code = _CODES.get(x.dtype)
-    if code is None:
-        _dtype_code(x)
-    if f.dtype != x.dtype:
-        raise TypeError("f and x must share one dtype")
-    return code, _gate(f, x.shape)
+def _native():
+    """The extension ``_mixer.so`` (raises if it is missing)."""
+    global _mixer
+    if _mixer is None:
+        lib()  # raises if libkla.so, which it is linked to, is missing
+        try:
+            from . import _mixer as module
+        except ImportError as e:
+            raise RuntimeError("the binding of the mixer operators is not built; build it with "
+                               "`python -m kalman_linear_attention_b200._build`") from e
+        module.set_error(KlaError)
+        _mixer = module
+    return _mixer
 
 
 def gated_scan_forward(f: torch.Tensor, x: torch.Tensor, h0: Optional[torch.Tensor] = None, *,
@@ -737,22 +688,7 @@ def gated_scan_forward(f: torch.Tensor, x: torch.Tensor, h0: Optional[torch.Tens
     [B, H, N] fp32 (None: zero).  Returns the states, fp32 [B, T, H, N]; the
     last one continues with gated_scan_step.  Enqueued on ``stream`` (default:
     the current stream) without synchronising."""
-    shape = x.shape
-    if len(shape) != 4:
-        raise ValueError("x must be [B, T, H, N]")
-    B, T, H, N = shape
-    code, gate = _gates_and_inputs(f, x)
-    index = x.get_device()
-    pf, px = _need("f", f, f.shape, x.dtype, index), _need("x", x, shape, x.dtype, index)
-    ph0, ph = _need("h0", h0, (B, H, N), torch.float32, index), _need("out", out, shape, torch.float32, index)
-
-    def call(handle):
-        h = out if out is not None else torch.empty_like(x, dtype=torch.float32)
-        _check(lib().kla_gated_scan_forward(pf, px, code, gate, ph0, ph or h.data_ptr(), B, T, H, N, handle),
-               "kla_gated_scan_forward")
-        return h
-
-    return _enqueue(index, stream, call)
+    return (_mixer or _native()).gated_scan_forward(f, x, h0, out, stream)
 
 
 def gated_scan_step(f: torch.Tensor, x: torch.Tensor, h_state: torch.Tensor, *,
@@ -761,26 +697,7 @@ def gated_scan_step(f: torch.Tensor, x: torch.Tensor, h_state: torch.Tensor, *,
     """One decode token of the gated recurrence (kla_gated_scan_step): x
     [B, H, N], f of that shape or [B, H], h_state [B, H, N] fp32.  The new state
     goes to ``out``, or in place to h_state without it; returns where it went."""
-    if out is None:
-        out = h_state
-    shape, dtype, index = x.shape, x.dtype, x.get_device()
-    f_shape = f.shape
-    # a decode step takes a few microseconds: one test for what is as it should be
-    if (len(shape) != 3 or dtype not in _CODES or f.dtype != dtype or (f_shape != shape and f_shape != shape[:-1])
-            or h_state.shape != shape or out.shape != shape or h_state.dtype != torch.float32
-            or out.dtype != torch.float32 or f.get_device() != index or h_state.get_device() != index
-            or out.get_device() != index or not f.is_contiguous() or not x.is_contiguous()
-            or not h_state.is_contiguous() or not out.is_contiguous()):
-        if len(shape) != 3:
-            raise ValueError("x must be [B, H, N]")
-        _gates_and_inputs(f, x)
-        _need("f", f, f_shape, dtype, index), _need("x", x, shape, dtype, index)
-        _need("h_state", h_state, shape, torch.float32, index), _need("out", out, shape, torch.float32, index)
-    B, H, N = shape
-    args = (f.data_ptr(), x.data_ptr(), _CODES[dtype], KLA_GATE_CHANNEL if f_shape == shape else KLA_GATE_HEAD,
-            h_state.data_ptr(), out.data_ptr(), B, H, N)
-    _check(_enqueue(index, stream, lambda handle: lib().kla_gated_scan_step(*args, handle)), "kla_gated_scan_step")
-    return out
+    return (_mixer or _native()).gated_scan_step(f, x, h_state, out, stream)
 
 
 def gated_scan_backward_workspace_size(B: int, T: int, H: int, N: int, dtype: torch.dtype = torch.float32,
@@ -800,31 +717,7 @@ def gated_scan_backward(f: torch.Tensor, h: torch.Tensor, g_h: torch.Tensor, h0:
     h0 as given to it, h the states it returned, g_h the loss gradient with
     respect to them (fp32).  Returns the gradients with respect to (f, x, h0):
     the first two in f's dtype, the last fp32; None where ``want`` is False."""
-    shape = h.shape
-    if len(shape) != 4:
-        raise ValueError("h must be the forward output, [B, T, H, N]")
-    B, T, H, N = shape
-    gate = _gate(f, shape)
-    code = _dtype_code(f)
-    index = h.get_device()
-    args = (_need("f", f, f.shape, f.dtype, index), code, gate, _need("h0", h0, (B, H, N), torch.float32, index),
-            _need("h", h, shape, torch.float32, index), _need("g_h", g_h, shape, torch.float32, index))
-    pw, nw = _need_workspace(workspace, index)
-
-    def call(handle):
-        gf = torch.empty_like(f) if want[0] else None
-        gx = torch.empty_like(h, dtype=f.dtype) if want[1] else None
-        gh0 = h.new_empty((B, H, N)) if want[2] else None
-        ws, n = pw, nw
-        if ws is None and gate == KLA_GATE_HEAD and want[0]:
-            n = gated_scan_backward_workspace_size(B, T, H, N, f.dtype, True)
-            room = torch.empty(n, dtype=torch.uint8, device=h.device) if n else None
-            ws = _ptr(room)
-        _check(lib().kla_gated_scan_backward(*args, _ptr(gf), _ptr(gx), _ptr(gh0), B, T, H, N, ws, n, handle),
-               "kla_gated_scan_backward")
-        return gf, gx, gh0
-
-    return _enqueue(index, stream, call)
+    return (_mixer or _native()).gated_scan_backward(f, h, g_h, h0, *want, workspace, stream)
 
 
 class GatedScan(torch.autograd.Function):
@@ -891,55 +784,6 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "n
     return inv_freq.to(device) if device is not None else inv_freq, scale
 
 
-_I64x3 = ctypes.c_int64 * 3
-
-
-def _head_rows(name: str, t: torch.Tensor, dtype: torch.dtype, index: int):
-    """The host array of the strides of [B, T, H, D] rows (None: dense)."""
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on the device of the other tensors; it is on {t.device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.is_contiguous():
-        return None
-    sb, st, sh, sd = t.stride()
-    if sd != 1 and t.shape[3] > 1:
-        raise ValueError(f"the last axis of {name} must be contiguous")
-    return _I64x3(sb, st, sh)
-
-
-def _rotation(index: int, B: int, T: int, D: int, inv_freq: Optional[torch.Tensor],
-              positions: Optional[torch.Tensor]):
-    """(inv_freq pointer, rot_dim, positions pointer, batch stride)."""
-    if inv_freq is None:
-        if positions is not None:
-            raise ValueError("positions need inv_freq")
-        return None, 0, None, 0
-    if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > D:
-        raise ValueError(f"inv_freq must be [rot_dim / 2] with rot_dim at most {D}, got {list(inv_freq.shape)}")
-    half = inv_freq.shape[0]
-    freq = _need("inv_freq", inv_freq, (half,), torch.float64, index)
-    if positions is None:
-        return freq, 2 * half, None, 0
-    if positions.dtype != torch.int64:
-        raise TypeError(f"positions must be torch.int64, got {positions.dtype}")
-    if positions.get_device() != index:
-        raise ValueError(f"positions must be on the device of the other tensors; they are on {positions.device}")
-    if positions.shape == (B, T):
-        batch = positions.stride(0) if B > 1 else 0
-    elif positions.shape == (T,):
-        batch = 0
-    else:
-        raise ValueError(f"positions must be [{B}, {T}] or [{T}], got {list(positions.shape)}")
-    if T > 1 and positions.stride(-1) != 1:
-        raise ValueError("the last axis of positions must be contiguous")
-    return freq, 2 * half, positions.data_ptr(), batch
-
-
-def _empty_rows(like: torch.Tensor) -> torch.Tensor:
-    return torch.empty_like(like, memory_format=torch.contiguous_format)
-
-
 def rotary_forward(x: torch.Tensor, inv_freq: torch.Tensor, positions: Optional[torch.Tensor] = None, *,
                    position0: int = 0, interleaved: bool = False, scale: float = 1.0, inverse: bool = False,
                    out: Optional[torch.Tensor] = None,
@@ -950,23 +794,8 @@ def rotary_forward(x: torch.Tensor, inv_freq: torch.Tensor, positions: Optional[
     (rotary_frequencies); positions int64 [B, T] or [T], or None for position0
     + t; ``interleaved``: neighbours form a pair, else the two halves do;
     ``inverse``: the other way round.  Returns a dense tensor of x's type."""
-    shape = x.shape
-    if len(shape) != 4:
-        raise ValueError("x must be [B, T, H, D]")
-    B, T, H, D = shape
-    code = _dtype_code(x)
-    index = x.get_device()
-    strides = _head_rows("x", x, x.dtype, index)
-    freq, rot, pos, batch = _rotation(index, B, T, D, inv_freq, positions)
-    po = _need("out", out, shape, x.dtype, index)
-
-    def call(handle):
-        y = out if out is not None else _empty_rows(x)
-        _check(lib().kla_rotary_forward(x.data_ptr(), strides, code, freq, rot, interleaved, scale, inverse, pos, batch,
-                                        position0, po or y.data_ptr(), B, T, H, D, handle), "kla_rotary_forward")
-        return y
-
-    return _enqueue(index, stream, call)
+    return (_mixer or _native()).rotary_forward(x, inv_freq, positions, position0, interleaved, scale, inverse, out,
+                                                stream)
 
 
 class Rotary(torch.autograd.Function):
@@ -991,26 +820,6 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions: Optional[torch.Te
     return Rotary.apply(x, inv_freq, positions, position0, interleaved, scale)
 
 
-def _qk_call(q: torch.Tensor, k: torch.Tensor, q_weight, k_weight, eps, inv_freq, positions, position0,
-             interleaved, scale):
-    """(device, sizes, the C arguments up to position0) of a QK-Norm call."""
-    qs, ks = q.shape, k.shape
-    if len(qs) != 4 or len(ks) != 4:
-        raise ValueError("q must be [B, T, Hq, D] and k [B, T, Hk, D]")
-    B, T, Hq, D = qs
-    Bk, Tk, Hk, Dk = ks
-    if B != Bk or T != Tk or D != Dk:
-        raise ValueError("q must be [B, T, Hq, D] and k [B, T, Hk, D]")
-    dtype, index = q.dtype, q.get_device()
-    code = _dtype_code(q)
-    q_strides, k_strides = _head_rows("q", q, dtype, index), _head_rows("k", k, dtype, index)
-    freq, rot, pos, batch = _rotation(index, B, T, D, inv_freq, positions)
-    return index, (B, T, Hq, Hk, D), (
-        q.data_ptr(), q_strides, k.data_ptr(), k_strides, code,
-        _need("q_weight", q_weight, (D,), torch.float32, index),
-        _need("k_weight", k_weight, (D,), torch.float32, index), eps, freq, rot, interleaved, scale, pos, batch, position0)
-
-
 def qk_norm_rotary_forward(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
                            k_weight: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
                            positions: Optional[torch.Tensor] = None, *, position0: int = 0, eps: float = 1e-6,
@@ -1023,18 +832,9 @@ def qk_norm_rotary_forward(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[
     RMS norm of each head, times the weight ([D] fp32 or None), rotated as in
     rotary_forward (not at all without inv_freq).  Returns dense (q, k) of the
     inputs' type."""
-    index, sizes, args = _qk_call(q, k, q_weight, k_weight, eps, inv_freq, positions, position0, interleaved, scale)
     q_out, k_out = (None, None) if out is None else out
-    pq, pk = _need("out", q_out, q.shape, q.dtype, index), _need("out", k_out, k.shape, q.dtype, index)
-
-    def call(handle):
-        yq = q_out if q_out is not None else _empty_rows(q)
-        yk = k_out if k_out is not None else _empty_rows(k)
-        _check(lib().kla_qk_norm_rotary_forward(*args, pq or yq.data_ptr(), pk or yk.data_ptr(), *sizes, handle),
-               "kla_qk_norm_rotary_forward")
-        return yq, yk
-
-    return _enqueue(index, stream, call)
+    return (_mixer or _native()).qk_norm_rotary_forward(q, k, q_weight, k_weight, inv_freq, positions, position0, eps,
+                                                        interleaved, scale, q_out, k_out, stream)
 
 
 def qk_norm_rotary_backward_workspace_size(Hq: int, Hk: int, D: int) -> int:
@@ -1057,26 +857,8 @@ def qk_norm_rotary_backward(q: torch.Tensor, k: torch.Tensor, g_q: Optional[torc
     k_weight): the first two dense in the inputs' type, the weights' fp32;
     None where ``want`` is False, where there is no weight, or where the
     output's gradient is None."""
-    index, sizes, args = _qk_call(q, k, q_weight, k_weight, eps, inv_freq, positions, position0, interleaved, scale)
-    pg = _need("g_q", g_q, q.shape, q.dtype, index), _need("g_k", g_k, k.shape, q.dtype, index)
-    pw, nw = _need_workspace(workspace, index)
-    want_q, want_k = want[0] and g_q is not None, want[1] and g_k is not None
-    want_qw = want[2] and g_q is not None and q_weight is not None
-    want_kw = want[3] and g_k is not None and k_weight is not None
-
-    def call(handle):
-        gq, gk = _empty_rows(q) if want_q else None, _empty_rows(k) if want_k else None
-        gqw, gkw = torch.empty_like(q_weight) if want_qw else None, torch.empty_like(k_weight) if want_kw else None
-        ws, n = pw, nw
-        if ws is None and (want_qw or want_kw):
-            n = qk_norm_rotary_backward_workspace_size(*sizes[2:])
-            room = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-            ws = _ptr(room)
-        _check(lib().kla_qk_norm_rotary_backward(*args, *pg, _ptr(gq), _ptr(gk), _ptr(gqw), _ptr(gkw), *sizes, ws, n,
-                                                 handle), "kla_qk_norm_rotary_backward")
-        return gq, gk, gqw, gkw
-
-    return _enqueue(index, stream, call)
+    return (_mixer or _native()).qk_norm_rotary_backward(q, k, q_weight, k_weight, inv_freq, positions, position0, eps,
+                                                         interleaved, scale, g_q, g_k, *want, workspace, stream)
 
 
 class QKNormRotary(torch.autograd.Function):
