@@ -520,7 +520,9 @@ kla_gated_forward_kernel(const GatedParams prm) {
         ask_next();
         copies_wait<Stage::ROUNDS - 1>();
         __syncwarp();
-        whole && left >= R ? run(Yes{}, buf, (int)(r & 1), first, left) : run(No{}, buf, (int)(r & 1), first, left);
+        // all warps of a CTA take the same branch: its barriers stand in both
+        whole && left >= (W - w) * R ? run(Yes{}, buf, (int)(r & 1), first, left)
+                                     : run(No{}, buf, (int)(r & 1), first, left);
         buf = buf == Stage::ROUNDS - 1 ? 0 : buf + 1;
     }
 }
@@ -636,9 +638,8 @@ kla_gated_backward_kernel(const GatedBackwardParams prm) {
         copies_commit();
     };
     // FULL: as in the forward kernel, with the tokens before and after
-    auto is_full = [&](int64_t left) { return whole && left < g.T && left > R; };
     auto ask = [&](int buf, int64_t first, const Tin *gate_rows, int64_t left) {
-        is_full(left) ? ask_rows(Yes{}, buf, first, gate_rows, left) : ask_rows(No{}, buf, first, gate_rows, left);
+        whole && left < g.T && left > R ? ask_rows(Yes{}, buf, first, gate_rows, left) : ask_rows(No{}, buf, first, gate_rows, left);
     };
     auto run = [&](auto full_, int buf, int parity, int64_t first, int64_t left_of_warp) {
         constexpr bool FULL = decltype(full_)::value;
@@ -777,7 +778,9 @@ kla_gated_backward_kernel(const GatedBackwardParams prm) {
         ask_next();
         copies_wait<Stage::ROUNDS - 1>();
         __syncwarp();
-        is_full(left) ? run(Yes{}, buf, (int)(r & 1), first, left) : run(No{}, buf, (int)(r & 1), first, left);
+        // all warps of a CTA take the same branch: its barriers stand in both
+        whole && left + w * R < g.T && left > (W - w) * R ? run(Yes{}, buf, (int)(r & 1), first, left)
+                                                          : run(No{}, buf, (int)(r & 1), first, left);
         buf = buf == Stage::ROUNDS - 1 ? 0 : buf + 1;
     }
 }
