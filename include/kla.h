@@ -521,7 +521,7 @@ kla_status_t kla_scan_forward_lti_plan(int64_t B, int64_t T, int64_t H, int64_t 
  *
  * Any real gate is allowed, 0 (the state starts afresh: sequences packed one
  * after another) and negative ones among them.  The magnitude of the product
- * of the gates of any 256 consecutive tokens must stay below 2^127 (it can
+ * of the gates of any 1024 consecutive tokens must stay below 2^127 (it can
  * exceed that only where gates are above 1), and the states within fp32
  * range; an input that is not finite makes the states from its token on
  * undefined, in its channel only.  States and arithmetic are fp32.  Any size
@@ -609,7 +609,7 @@ kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype, kla_ga
  *                  gradient of x from the gradient of the output)
  *   out            [B, T, H, D] dense, dtype (written, rounded once)
  *
- * 0 <= rot_dim <= D <= KLA_ROTARY_MAX_D, rot_dim even, any alignment; arrays
+ * 0 <= rot_dim <= D <= KLA_ROTARY_MAX_D, rot_dim even, H * D < 2^31, any alignment; arrays
  * and strides that allow 16-byte vectors are fastest.  An empty problem is
  * valid.  out may not overlap the inputs.
  */
@@ -629,7 +629,7 @@ kla_status_t kla_rotary_forward(const void *x, const int64_t *x_strides, kla_dty
  *                    projection, say); Hk may be 0 and k NULL then
  *   q_weight, k_weight
  *                    [D] fp32, or NULL for 1
- *   eps              >= 0
+ *   eps              >= 0 (with 0, a row of zeros has no norm: NaN)
  *   q_out, k_out     dense, dtype (rounded once)
  *
  * The k and q of kla_layer_forward / kla_layer_step are such rows with D = Ns.

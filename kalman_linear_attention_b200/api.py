@@ -14,6 +14,7 @@ import os
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(_HERE, "libkla.so")
@@ -723,7 +724,9 @@ def gated_scan_backward(f: torch.Tensor, h: torch.Tensor, g_h: torch.Tensor, h0:
 class GatedScan(torch.autograd.Function):
     """Differentiable gated recurrence: forward = kla_gated_scan_forward,
     backward = kla_gated_scan_backward.  Inputs (f, x, h0) as in
-    gated_scan_forward; returns the states."""
+    gated_scan_forward; returns the states.  (To capture a backward pass into a
+    CUDA graph, let go of every eager graph over the same leaves first: torch
+    would join the stream that they were made on to the capture.)"""
 
     @staticmethod
     def forward(ctx, f, x, h0):
@@ -732,6 +735,7 @@ class GatedScan(torch.autograd.Function):
         return h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_h):
         f, h, h0 = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -808,6 +812,7 @@ class Rotary(torch.autograd.Function):
         return rotary_forward(x, inv_freq, positions, **ctx.rotation)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         inv_freq, positions = ctx.saved_tensors
         return (rotary_forward(g.contiguous(), inv_freq, positions, inverse=True, **ctx.rotation),
@@ -873,6 +878,7 @@ class QKNormRotary(torch.autograd.Function):
         return qk_norm_rotary_forward(q, k, q_weight, k_weight, inv_freq, positions, **ctx.options)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_q, g_k):
         q, k, *rest = ctx.saved_tensors
         grads = [None if g is None else g.contiguous() for g in (g_q, g_k)]

@@ -63,7 +63,7 @@ kla_status_t check_call(kla_dtype_t dtype, const double *inv_freq, int64_t rot_d
 bool set_input(const Call &c, const void *x, const int64_t *strides, int64_t heads, RotaryTensor *t, int64_t *bytes) {
     if (heads < 0 || heads > INT32_MAX) return false;
     int64_t row = 0, batch = 0, all = 0, span = 0;
-    if (!mul_ok(heads, c.D, &row) || !mul_ok(row, c.T, &batch) || !mul_ok(batch, c.B, &all) || !mul_ok(all, 4, &span))
+    if (!mul_ok(heads, c.D, &row) || row > INT32_MAX || !mul_ok(row, c.T, &batch) || !mul_ok(batch, c.B, &all) || !mul_ok(all, 4, &span))
         return false;
     t->x = x;
     t->heads = (int)heads;

@@ -335,3 +335,96 @@ def test_offsets_past_32_bits():
                               HALF_STEP[torch.bfloat16])
     assert_within(gx[sl], *want["x"], "last gradients of x")
     assert_within(gf[sl], *want["f"], "last gradients of f")
+
+
+@pytest.mark.parametrize("gate", ["channel", "head"])
+def test_gates_above_one(gate):
+    """Gates that grow the state a little, over spans that clusters compose."""
+    kla = _kla()
+    shape = (1, 2600, 1, 64)
+    f, x, g, h0 = _inputs(shape, torch.float32, gate, True, seed=15)
+    f = 0.99 + 0.02 * torch.rand(f.shape, generator=torch.Generator().manual_seed(1))
+    df, dx, dg, dh0 = to_device(f, x, g, h0)
+    h = kla.gated_scan_forward(df, dx, dh0)
+    assert_within(h, *reference(_np(f), _np(x), _np(h0)), "h")
+    want = reference_backward(_np(f), _np(h), _np(g), _np(h0), HALF_STEP[torch.float32])
+    for name, got in zip(("f", "x", "h0"), kla.gated_scan_backward(df, h, dg, dh0)):
+        assert_within(got, *want[name], f"gradient of {name}")
+
+
+def test_given_outputs_and_workspaces():
+    kla = _kla()
+    f, x, g, h0 = to_device(*_inputs((2, 60, 2, 48), torch.bfloat16, "head", True, seed=17))
+    out = torch.full(x.shape, float("nan"), device=DEV)
+    assert kla.gated_scan_forward(f, x, h0, out=out) is out
+    want = kla.gated_scan_backward(f, out, g, h0)
+    n = kla.gated_scan_backward_workspace_size(2, 60, 2, 48, torch.bfloat16, True)
+    room = torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+    for a, b in zip(want, kla.gated_scan_backward(f, out, g, h0, workspace=room)):
+        assert torch.equal(a, b)
+    with pytest.raises(kla.KlaError) as e:
+        kla.gated_scan_backward(f, out, g, h0, workspace=room[:256])
+    assert e.value.status == 3
+    flat = out.view(-1)
+    with pytest.raises(kla.KlaError) as e:
+        kla.gated_scan_step(f[:, 0].contiguous(), x[:, 0].contiguous(), flat[:192].view(2, 2, 48),
+                            out=flat[96:288].view(2, 2, 48))
+    assert e.value.status == 1  # neither in place nor apart
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams do not share anything."""
+    kla = _kla()
+    sets = [to_device(*_inputs((1, 4000, 2, 96), torch.float32, "head", True, seed=s)) for s in (21, 22)]
+    want = []
+    for f, x, g, h0 in sets:
+        h = kla.gated_scan_forward(f, x, h0)
+        want.append((h, *kla.gated_scan_backward(f, h, g, h0)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for k, (f, x, g, h0) in enumerate(sets):
+            with torch.cuda.stream(streams[k]):
+                h = kla.gated_scan_forward(f, x, h0)
+                got[k].append((h, *kla.gated_scan_backward(f, h, g, h0)))
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for one in got[k]:
+            for a, b in zip(one, want[k]):
+                assert torch.equal(a, b)
+
+
+def test_captured_training_step_and_second_derivatives():
+    """Forward and backward through autograd in one graph, replayed; a second
+    derivative is refused."""
+    kla = _kla()
+    f, x, g, h0 = to_device(*_inputs((2, 80, 2, 32), torch.float32, "head", True, seed=23))
+    leaves = [t.clone().requires_grad_() for t in (f, x, h0)]
+
+    def step():
+        for t in leaves:
+            t.grad = None
+        (kla.gated_scan(*leaves) * g).sum().backward()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    with torch.no_grad():
+        for t, new in zip(leaves, to_device(*_inputs((2, 80, 2, 32), torch.float32, "head", True, seed=24))[:2]):
+            t.copy_(new)
+    graph.replay()
+    torch.cuda.synchronize()
+    h = kla.gated_scan_forward(*(t.detach() for t in leaves))
+    for leaf, want in zip(leaves, kla.gated_scan_backward(leaves[0].detach(), h, g, leaves[2].detach())):
+        assert torch.equal(leaf.grad, want)
+    once = f.clone().requires_grad_()
+    first, = torch.autograd.grad((kla.gated_scan(once, x) * g).sum(), once, create_graph=True)
+    with pytest.raises(RuntimeError):
+        first.sum().backward()
