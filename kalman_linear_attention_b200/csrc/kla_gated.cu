@@ -4,6 +4,7 @@
 #include "kla_gated.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace {
 
@@ -28,30 +29,32 @@ bool sizes(int64_t B, int64_t T, int64_t H, int64_t N, kla_gate_t gate, Sizes *s
 // Tokens of a lane in a round: as many as make 4 to 8 KB of a warp's rows in
 // flight (two channels a lane).  Forward, half as many: the long fp32 shape
 // (B=1, T=65536, 32 x 128) 580 us against 659 with 16 tokens; shared gates
-// 456 us with 16 against 508 with 8.  Backward: B=8, T=2048, 16 x 128 fp32 108 us
-// against 124 with 8; bf16 80 us with 8 against 85 with 4; shared gates, the
-// long fp32 shape, 822 us with 16 against 910 with 8.
-#ifndef KLA_GATED_L
-#define KLA_GATED_L 0
-#endif
+// 456 us with 16 against 508 with 8.  bf16 gates of each channel: where an SM
+// has one CTA at most (`few`: no more tiles than SMs), T=32768, 32 x 128, 195 us
+// with 16, 204 with 12; where it has more, B=8, T=2048, 16 x 128, 49.6 us with
+// 12, 51.5 with 16.  Backward: B=8, T=2048, 16 x 128 fp32 108 us against 124
+// with 8; bf16 80 us with 8 against 85 with 4; shared gates, the long fp32
+// shape, 822 us with 16 against 910 with 8.
 template <typename Tin, bool HEAD, bool BACKWARD>
-constexpr int tokens_of_lane() {
-    if (KLA_GATED_L > 0) return KLA_GATED_L;
+constexpr int tokens_of_lane(bool few) {
     if (HEAD) return 16;
-    return BACKWARD && sizeof(Tin) == 4 ? 4 : 8;
+    if (BACKWARD) return sizeof(Tin) == 4 ? 4 : 8;
+    return sizeof(Tin) == 4 ? 8 : few ? 16 : 12;
 }
-int tokens_of_lane(kla_dtype_t dt, bool head, bool backward) {
+int tokens_of_lane(kla_dtype_t dt, bool head, bool backward, bool few) {
+    using bf16 = __nv_bfloat16;
     if (dt == KLA_F32)
-        return head ? backward ? tokens_of_lane<float, true, true>() : tokens_of_lane<float, true, false>()
-                    : backward ? tokens_of_lane<float, false, true>() : tokens_of_lane<float, false, false>();
-    return head ? backward ? tokens_of_lane<__nv_bfloat16, true, true>() : tokens_of_lane<__nv_bfloat16, true, false>()
-                : backward ? tokens_of_lane<__nv_bfloat16, false, true>() : tokens_of_lane<__nv_bfloat16, false, false>();
+        return head ? backward ? tokens_of_lane<float, true, true>(few) : tokens_of_lane<float, true, false>(few)
+                    : backward ? tokens_of_lane<float, false, true>(few) : tokens_of_lane<float, false, false>(few);
+    return head ? backward ? tokens_of_lane<bf16, true, true>(few) : tokens_of_lane<bf16, true, false>(few)
+                : backward ? tokens_of_lane<bf16, false, true>(few) : tokens_of_lane<bf16, false, false>(few);
 }
 
 struct Launch {
     GatedTiles g;
     int64_t tiles;
     int vec, S, copy, W, C, group;
+    bool few;  // no more tiles than SMs
 };
 
 // The arrays of a call: those whose rows are read through shared memory
@@ -90,16 +93,37 @@ int copy_of(int64_t HN, int64_t seg, const Array *arrays, int n) {
     return start ? wide ? WIDE : SHIFT : NARROW;
 }
 
+// Warps that an SM holds at once, by registers and by shared memory
+// (rows and gates of a warp, as GatedStage has them).
+struct Resident {
+    kla_dtype_t dt;
+    bool head, backward;
+    int64_t tokens(bool few) const { return tokens_of_lane(dt, head, backward, few); }
+    // bytes of a warp's rows in one round
+    int64_t stage(const Launch &l) const {
+        const int64_t e = dtype_size(dt), L = tokens(l.few), S = l.S;
+        const int64_t pad = l.copy == SHIFT ? 16 : 0, cw = 32 / S * l.vec, apart = S > 1 ? cw : 0;
+        const int64_t wide = S * (L * (4 * cw + pad) + 4 * apart), in = S * (L * (e * cw + pad) + e * apart);
+        return (backward ? 2 * wide : in) + (head ? 0 : in);
+    }
+    int64_t warps(const Launch &l) const {
+        const int64_t bytes =
+            kGatedRounds * stage(l) + (head ? tokens(l.few) * kGatedHeads * 4 : 0) + 512 * l.vec;
+        return std::min<int64_t>(65536 / (32 * (backward ? KLA_GATED_BACKWARD_REGS : KLA_GATED_REGS)) / 4 * 4,
+                                 226 * 1024 / bytes);
+    }
+};
+
 // The widest tiles of which there are enough: 0.8 of the SMs (shared gates,
 // the long fp32 shape: 128 tiles of 32 channels 424 us, 256 of 16 455; B=2, T=5001,
 // 12 x 80, 21 us against 27), or 1.5 of them with one channel a lane.  Rows that start
 // on 16 bytes, and on pairs of channels in every array, take two channels a
 // lane (half the instructions for a channel, and two chains of multiply-adds
 // side by side), others one; a warp's lanes in 1, 2, 4 or 8 parts.
-// resident(vec, S, copy): warps that an SM holds.
 template <typename F>
-Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, bool head, int L, const Array *arrays, int n, F resident) {
+Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, const Array *arrays, int n, const F &resident) {
     Launch l;
+    const bool head = resident.head;
     const int64_t HN = H * N, sms = sm_count();
     l.g.T = T; l.g.H = H; l.g.N = N; l.g.HN = HN;
     bool pairs = HN % 2 == 0 && (!head || N % 2 == 0);
@@ -114,25 +138,27 @@ Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, bool head, int L, const 
         if (vec == 2 ? !pairs || k.copy != WIDE : any) continue;
         if (vec == 1 && k.copy == WIDE) k.copy = SHIFT;
         // parts no shorter than a sector of memory a row
+        k.few = k.tiles <= sms;
+        const int64_t L = resident.tokens(k.few);
         if (S > 1 && (k.copy == NARROW || (T + L - 1) / L < S || (vec == 2 && 64 / S * arrays[0].size < 32)))
             continue;
         l = k;
         any = any || vec == 2;
         if (vec == 2 ? 5 * l.tiles >= 4 * sms : 2 * l.tiles >= 3 * sms) break;
     }
-    const int64_t chunks = (T + l.S * L - 1) / (l.S * L);  // of a warp
-    const int64_t held = resident(l.vec, l.S, l.copy);
+    const int64_t R = l.S * resident.tokens(l.few), chunks = (T + R - 1) / R;  // of a warp
+    const int64_t held = resident.warps(l);
     l.C = 1;
     l.W = (int)std::min({(int64_t)8, held, chunks});
     if (3 * l.tiles <= 2 * sms) {
         // few tiles all the same: clusters, until there are two CTAs for each SM
         while (l.C < kGatedMaxCluster && l.tiles * l.C <= sms && (int64_t)l.C * l.W < chunks) l.C *= 2;
-    } else if (l.tiles <= sms && chunks >= 32 * kGatedMaxWarps) {
+    } else if (l.few && chunks >= 32 * kGatedMaxWarps) {
         // one CTA an SM, and a long sequence: as many warps as have 64 KB of
         // rows in a round (the long fp32 shape: 515 us with 16 against 608
         // with 8; backward 922 against 1132)
         l.W = (int)std::max<int64_t>(
-            l.W, std::min({(int64_t)kGatedMaxWarps, held, 64 * 1024 / resident.stage(l.vec, l.S, l.copy)}));
+            l.W, std::min({(int64_t)kGatedMaxWarps, held, 64 * 1024 / resident.stage(l)}));
     }
     // many tiles: fewer warps each, so that all are resident at once (CTAs
     // that had to wait for others would run alone at the end)
@@ -190,15 +216,21 @@ cudaError_t run(const Launch &l, int stage, const Params &prm, cudaStream_t st) 
     return launch(KERNEL, l.tiles * l.C, 32 * l.W, l.C, (size_t)smem_bytes<VEC>(stage, l.W, l.C), st, prm);
 }
 
-template <typename Tin, int VEC, int S, bool HEAD, int COPY>
-cudaError_t run_scan(const Launch &l, const GatedParams &prm, cudaStream_t st) {
-    constexpr int L = tokens_of_lane<Tin, HEAD, false>(), STAGE = GatedStage<Tin, VEC, S, HEAD, L, COPY, false>::WARP;
+template <typename Tin, int VEC, int S, bool HEAD, int COPY, int L>
+cudaError_t run_tokens(const Launch &l, const GatedParams &prm, cudaStream_t st) {
+    constexpr int STAGE = GatedStage<Tin, VEC, S, HEAD, L, COPY, false>::WARP;
     return run<kla_gated_forward_kernel<Tin, VEC, S, HEAD, L, COPY>, VEC>(l, STAGE, prm, st);
 }
-template <typename Tin, int VEC, int S, bool HEAD, int COPY>
-cudaError_t run_scan(const Launch &l, const GatedBackwardParams &prm, cudaStream_t st) {
-    constexpr int L = tokens_of_lane<Tin, HEAD, true>(), STAGE = GatedStage<Tin, VEC, S, HEAD, L, COPY, true>::WARP;
+template <typename Tin, int VEC, int S, bool HEAD, int COPY, int L>
+cudaError_t run_tokens(const Launch &l, const GatedBackwardParams &prm, cudaStream_t st) {
+    constexpr int STAGE = GatedStage<Tin, VEC, S, HEAD, L, COPY, true>::WARP;
     return run<kla_gated_backward_kernel<Tin, VEC, S, HEAD, L, COPY>, VEC>(l, STAGE, prm, st);
+}
+template <typename Tin, int VEC, int S, bool HEAD, int COPY, typename Params>
+cudaError_t run_scan(const Launch &l, const Params &prm, cudaStream_t st) {
+    constexpr bool BACKWARD = std::is_same_v<Params, GatedBackwardParams>;
+    return l.few ? run_tokens<Tin, VEC, S, HEAD, COPY, tokens_of_lane<Tin, HEAD, BACKWARD>(true)>(l, prm, st)
+                 : run_tokens<Tin, VEC, S, HEAD, COPY, tokens_of_lane<Tin, HEAD, BACKWARD>(false)>(l, prm, st);
 }
 // The forms that plan() chooses from.
 template <typename Tin, bool HEAD, typename Params>
@@ -218,25 +250,6 @@ cudaError_t run_type(const Launch &l, kla_dtype_t dt, bool head, const Params &p
     if (dt == KLA_F32) return head ? run_form<float, true>(l, prm, st) : run_form<float, false>(l, prm, st);
     return head ? run_form<__nv_bfloat16, true>(l, prm, st) : run_form<__nv_bfloat16, false>(l, prm, st);
 }
-
-// Warps that an SM holds at once, by registers and by shared memory (two
-// rounds of rows a warp, as GatedStage has them).
-struct Resident {
-    int64_t e, L;
-    bool head, backward;
-    // bytes of a warp's rows in one round
-    int64_t stage(int vec, int S, int copy) const {
-        const int64_t pad = copy == SHIFT ? 16 : 0, cw = 32 / S * vec, apart = S > 1 ? cw : 0;
-        const int64_t wide = S * (L * (4 * cw + pad) + 4 * apart), in = S * (L * (e * cw + pad) + e * apart);
-        return (backward ? 2 * wide : in) + (head ? 0 : in);
-    }
-    int64_t operator()(int vec, int S, int copy) const {
-        const int64_t rounds = e == 2 && !head && !backward ? 3 : 2;
-        const int64_t bytes = rounds * stage(vec, S, copy) + (head ? L * kGatedHeads * 4 : 0) + 512 * vec;
-        return std::min<int64_t>(65536 / (32 * (backward ? KLA_GATED_BACKWARD_REGS : KLA_GATED_REGS)) / 4 * 4,
-                                 226 * 1024 / bytes);
-    }
-};
 
 template <typename Tin>
 int step_vec(const GatedStepParams &prm, bool head) {
@@ -285,8 +298,7 @@ KLA_API kla_status_t kla_gated_scan_forward(const void *f, const void *x, kla_dt
     // a gate for each head of one channel is a gate for each channel
     const bool head = gate == KLA_GATE_HEAD && N > 1;
     const Array arrays[3] = {{x, e, true}, {h, 4, false}, {f, e, true}};
-    const int L = tokens_of_lane(in_dtype, head, false);
-    const Launch l = plan(B, T, H, N, head, L, arrays, head ? 2 : 3, Resident{e, L, head, false});
+    const Launch l = plan(B, T, H, N, arrays, head ? 2 : 3, Resident{in_dtype, head, false});
     if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
     GatedParams prm;
     prm.g = l.g;
@@ -362,8 +374,7 @@ KLA_API kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype
     const bool head = gate == KLA_GATE_HEAD && N > 1;
     const Array arrays[5] = {{g_h, 4, true}, {grad_f ? h : nullptr, 4, true}, {grad_x, e, false},
                              {f, e, true}, {grad_f, e, false}};
-    const int L = tokens_of_lane(in_dtype, head, true);
-    const Launch l = plan(B, T, H, N, head, L, arrays, head ? 3 : 5, Resident{e, L, head, true});
+    const Launch l = plan(B, T, H, N, arrays, head ? 3 : 5, Resident{in_dtype, head, true});
     if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
     const int64_t parts = head ? parts_of(N, 32 / l.S * l.vec) : 1;
     GatedBackwardParams prm;

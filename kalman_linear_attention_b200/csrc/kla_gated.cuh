@@ -53,13 +53,11 @@ namespace kla_mixer {
 #define KLA_GATED_WARPS 16
 #endif
 constexpr int kGatedMaxWarps = KLA_GATED_WARPS;
-// Rounds of rows that a warp holds: the present one, and one asked for; or two
-// asked for, of fewer tokens, forward with a bf16 gate for each channel (B=8,
-// T=2048, 16 x 128: 49 us against 52; fp32 took 76 us against 66 so).
-template <typename Tin, bool HEAD, bool BACKWARD>
-__host__ __device__ constexpr int gated_rounds() {
-    return sizeof(Tin) == 2 && !HEAD && !BACKWARD ? 3 : 2;
-}
+// Rounds of rows that a warp holds: the present one, and one asked for.  With
+// two asked for, of 8 tokens a lane, a bf16 gate for each channel took as long
+// for B=8, T=2048, 16 x 128 (49 us) and 227 us against 195 for B=1, T=32768,
+// 32 x 128; fp32 took 76 us against 66.
+constexpr int kGatedRounds = 2;
 // Registers of a thread, forward and backward: 24 and 16 warps on an SM.
 #ifndef KLA_GATED_REGS
 #define KLA_GATED_REGS 80
@@ -369,7 +367,7 @@ struct GatedStage {
     static constexpr int H = X + (BACKWARD ? Wide::BYTES : In::BYTES);  // rows of h
     static constexpr int F = H + (BACKWARD ? Wide::BYTES : 0);          // rows of f
     static constexpr int BYTES = F + (HEAD ? 0 : In::BYTES);
-    static constexpr int ROUNDS = gated_rounds<Tin, HEAD, BACKWARD>();
+    static constexpr int ROUNDS = kGatedRounds;
     static constexpr int GATES = ROUNDS * BYTES;
     static constexpr int WARP = GATES + (HEAD ? L * kGatedHeads * 4 : 0);
     static_assert(BYTES % 16 == 0 && WARP % 16 == 0, "16-byte pieces");
