@@ -12,14 +12,13 @@ namespace {
 
 using namespace kla_mixer;
 
-// (Overridable at build time for tuning sweeps.)
-#ifndef KLA_ROTARY_ROWS
-#define KLA_ROTARY_ROWS 8
-#endif
-
-#ifndef KLA_ROTARY_ITEMS
-#define KLA_ROTARY_ITEMS 2
-#endif
+// Heads of a token that a group of lanes takes one after another, with the
+// cos and sin that it holds (B=4, T=4096, 32 + 8 heads of 128, bf16: 69 us with
+// 8, 78 with 4, 70 with 16; 16 heads of 16: 146 us, 141 and 226), where there
+// are two items at least for each warp of a full GPU (B=8, T=2048, 16 + 16 heads
+// of 128: 56 us, 61 with four; the first shape's backward pass 103 us, 109
+// with one).
+constexpr int kRotaryRows = 8, kRotaryItems = 2;
 
 // What one call works on, checked: everything but the tensors.
 struct Call {
@@ -113,10 +112,11 @@ void choose_vec(Call *c, int tensors) {
     c->upl = (c->prm.units + lanes - 1) / lanes;
 }
 
-// How warps share a tensor's tokens and heads.  A group takes KLA_ROTARY_ROWS
+// How warps share a tensor's tokens and heads.  A group takes kRotaryRows
 // heads of a token where there are tokens enough to fill the SMs with warps,
-// fewer where there are not.  At most as many CTAs as are resident at once; the tensors share them by their rows and what an item costs beyond
-// its rows (about two rows' time: cos and sin, the first copies).
+// fewer where there are not.  At most as many CTAs as are resident at once;
+// the tensors share them by their rows and what an item costs beyond its rows
+// (about two rows' time: cos and sin, the first copies).
 void choose_items(Call *c, int tensors, bool backward) {
     const int64_t cap = (int64_t)sm_count() * rotary_resident(c->vec, c->upl, backward);
     const int64_t warps = kRotaryThreads / 32, abreast = 32 / c->prm.lanes;
@@ -129,11 +129,13 @@ void choose_items(Call *c, int tensors, bool backward) {
         // heads that a warp takes at once: few, so that a group has many heads
         // and cos and sin serve them all; more where warps would be idle
         int64_t n = 1;
-        while (n < abreast && n < h && (n * KLA_ROTARY_ROWS < h || c->prm.tokens * n < KLA_ROTARY_ITEMS * fill * abreast)) n *= 2;
+        while (n < abreast && n < h &&
+               (n * kRotaryRows < h || c->prm.tokens * n < kRotaryItems * fill * abreast))
+            n *= 2;
         t.abreast = (int)n;
         const int64_t shares = (c->prm.tokens + abreast / n - 1) / (abreast / n);
         const int64_t most = (h + n - 1) / n;  // one head a group
-        int64_t splits = (most + KLA_ROTARY_ROWS - 1) / KLA_ROTARY_ROWS;
+        int64_t splits = (most + kRotaryRows - 1) / kRotaryRows;
         splits = std::max(splits, std::min(most, fill / std::max<int64_t>(1, shares)));
         t.splits = (int)splits;
         const int64_t items = shares > kMaxGrid ? kMaxGrid : shares * splits;  // enough to fill any grid
@@ -219,7 +221,7 @@ Range positions_range(const Call &c, const int64_t *positions) {
 }
 
 // CTAs of a backward call at most.
-int64_t backward_cap() { return (int64_t)sm_count() * KLA_ROTARY_BACKWARD_MINB; }
+int64_t backward_cap() { return (int64_t)sm_count() * kRotaryBackwardCtas; }
 
 }  // namespace
 

@@ -16,7 +16,15 @@
 //   dL/dw_d = sum over rows of g'_d x_d r,
 //   dL/dx_d = r (u_d - x_d r^2 mean(u x)).
 //
-// Every element is read and written once: the kernels are bound by HBM.  A
+// Every element is read and written once, so HBM is the floor: 52 us for B=4,
+// T=4096, 32 + 8 heads of 128 in bf16, of which the norm with the rotation
+// takes 69 us (4.9 TB/s, 0.75 of a copy), its backward pass 103 (0.76), the
+// rotation of the queries alone 49 (0.84); fp32 rows reach 0.85.  Instructions
+// come next to it (0.58 to 0.67 of the issue slots): conversions, the products
+// with w and r, the turns and the exchanges of the sum of squares are a few
+// instructions for each pair of elements, which 4 bytes of traffic in bf16
+// leave little time for.  Rows of a few elements (D = 16: 0.57) pay for the
+// row's own work.  A
 // row belongs to a group of lanes (a power of two, at most a warp), and a
 // warp to one token, or to several where a token's heads do not fill it: its
 // lanes form the tokens' cos and sin together, in shared memory, and each
@@ -44,20 +52,17 @@
 namespace kla_mixer {
 
 constexpr int kRotaryThreads = 256;
-// CTAs per SM that the registers leave room for.
-#ifndef KLA_ROTARY_MINB
-#define KLA_ROTARY_MINB 3
-#endif
-// Rows in flight and in use (up to 16 elements a lane).
-#ifndef KLA_ROTARY_RING
-#define KLA_ROTARY_RING 3
-#endif
-#ifndef KLA_ROTARY_BACKWARD_MINB
-#define KLA_ROTARY_BACKWARD_MINB 2
-#endif
+// CTAs of an SM, by the registers that they leave a thread: 80 forward, 128
+// backward (the gradient's rows, and the weights' sums).  B=4, T=4096, 32 + 8
+// heads of 128, bf16: forward 69 us with 3, 71 with 2, 92 with 4 (spills);
+// backward 103 us with 2, 144 with 1, 218 with 3 (spills).
+constexpr int kRotaryCtas = 3, kRotaryBackwardCtas = 2;
+// Rows in flight and in use (up to 16 elements a lane): forward 69 us with 3,
+// 75 with 2, 69 with 4; backward 103, 109 and 105.
+constexpr int kRotaryRing = 3;
 
 __host__ __device__ constexpr int rotary_resident(int vec, int upl, bool backward) {
-    return vec * upl > 8 ? 1 : backward || upl > 1 ? KLA_ROTARY_BACKWARD_MINB : KLA_ROTARY_MINB;
+    return vec * upl > 8 ? 1 : backward || upl > 1 ? kRotaryBackwardCtas : kRotaryCtas;
 }
 
 struct RotaryTensor {
@@ -247,7 +252,7 @@ struct RotaryShared {
     static constexpr int BYTES = VEC * (int)sizeof(T);  // of a vector
     static constexpr bool ASYNC = BYTES >= 4;
     static constexpr int VECTORS = 2 * UPL * (BACKWARD ? 2 : 1);  // of a lane and row
-    static constexpr int RING = VEC * UPL > 8 ? 2 : KLA_ROTARY_RING;
+    static constexpr int RING = VEC * UPL > 8 ? 2 : kRotaryRing;
     static constexpr int SLOT = VECTORS * 32 * BYTES;
     static constexpr int TABLE_OFF = RING * SLOT;
     __host__ __device__ static constexpr int warp_bytes(int table_pairs) {
