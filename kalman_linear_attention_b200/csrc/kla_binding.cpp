@@ -159,9 +159,16 @@ PyObject *tuple(const T &...t) {
     ((PyTuple_SET_ITEM(o, i++, wrap(t))), ...);
     return o;
 }
+// A given tensor was written: autograd counts versions, and refuses to use what
+// it saved from before (such as the states that a view of them steps on from).
+void written(PyObject *o) {
+    const Tensor &t = THPVariable_Unpack(o);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 // The argument itself where it was given, else the new tensor.
 PyObject *given_or(PyObject *o, const Tensor &t) {
     if (o == Py_None) return wrap(t);
+    written(o);
     Py_INCREF(o);
     return o;
 }
@@ -225,8 +232,7 @@ PyObject *gated_scan_step(PyObject *const *a) {
     const Enqueue on(at, a[4]);
     check(kla_gated_scan_step(pf, px, code, gate, static_cast<const float *>(h), static_cast<float *>(ph), s[0], s[1], s[2],
                               on.handle), "kla_gated_scan_step");
-    Py_INCREF(out);
-    return out;
+    return given_or(out, Tensor());
 }
 
 // (f, h, g_h, h0, three of want, workspace, stream)

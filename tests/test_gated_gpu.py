@@ -428,3 +428,22 @@ def test_captured_training_step_and_second_derivatives():
     first, = torch.autograd.grad((kla.gated_scan(once, x) * g).sum(), once, create_graph=True)
     with pytest.raises(RuntimeError):
         first.sum().backward()
+
+
+def test_a_step_on_saved_states_is_noticed():
+    """Stepping in place on a view of the states that a backward pass needs is
+    an error there, not a wrong gradient; so is writing them through out=."""
+    kla = _kla()
+    shape = (1, 5, 2, 8)
+    f, x, _, _ = (None if t is None else t.float() for t in _inputs(shape, torch.float32, "channel", False))
+    f = f.cuda().requires_grad_()
+    x = x.cuda()
+    for write in (lambda h: kla.gated_scan_step(x[:, 0].contiguous(), x[:, 1].contiguous(), h.detach()[:, -1]),
+                  lambda h: kla.gated_scan_forward(f.detach(), x, out=h.detach())):
+        h = kla.gated_scan(f, x)
+        write(h)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            h.sum().backward()
+    with torch.inference_mode():  # tensors without versions
+        state = torch.zeros(1, 2, 8, device="cuda")
+        assert kla.gated_scan_step(x[:, 0].contiguous(), x[:, 1].contiguous(), state) is state
