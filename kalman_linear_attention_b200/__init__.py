@@ -2,7 +2,7 @@
 Attention (KLA).
 
 The compute path is the C-ABI CUDA library ``libkla.so`` (declared in
-``include/kla.h``); :mod:`.api` is its thin ctypes binding and is imported on
+``include/kla.h``); :mod:`.api` is its thin binding and is imported on
 first use, so that importing :mod:`.workloads` (seeded inputs) needs neither
 torch nor the built library.
 """
