@@ -609,7 +609,7 @@ kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype, kla_ga
  *                  gradient of x from the gradient of the output)
  *   out            [B, T, H, D] dense, dtype (written, rounded once)
  *
- * 0 <= rot_dim <= D <= KLA_ROTARY_MAX_D, rot_dim even, H * D < 2^31, any alignment; arrays
+ * 0 <= rot_dim <= D <= KLA_ROTARY_MAX_D, rot_dim even, H * D <= 2^29, any alignment; arrays
  * and strides that allow 16-byte vectors are fastest.  An empty problem is
  * valid.  out may not overlap the inputs.
  */

@@ -20,6 +20,8 @@ using namespace kla_mixer;
 // with one).
 constexpr int kRotaryRows = 8, kRotaryItems = 2;
 
+constexpr int64_t kMaxRow = 1 << 29;  // elements of a token
+
 // What one call works on, checked: everything but the tensors.
 struct Call {
     RotaryParams prm = {};
@@ -62,7 +64,9 @@ kla_status_t check_call(kla_dtype_t dtype, const double *inv_freq, int64_t rot_d
 bool set_input(const Call &c, const void *x, const int64_t *strides, int64_t heads, RotaryTensor *t, int64_t *bytes) {
     if (heads < 0 || heads > INT32_MAX) return false;
     int64_t row = 0, batch = 0, all = 0, span = 0;
-    if (!mul_ok(heads, c.D, &row) || row > INT32_MAX || !mul_ok(row, c.T, &batch) || !mul_ok(batch, c.B, &all) || !mul_ok(all, 4, &span))
+    // heads and elements of a token are counted in 32 bits, up to two steps past the last
+    if (!mul_ok(heads, c.D, &row) || row > kMaxRow || !mul_ok(row, c.T, &batch) || !mul_ok(batch, c.B, &all) ||
+        !mul_ok(all, 4, &span))
         return false;
     t->x = x;
     t->heads = (int)heads;

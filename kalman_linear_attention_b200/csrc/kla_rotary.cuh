@@ -43,8 +43,9 @@
 // shared memory took 1.2 to 2.4 times as long as narrow ones.)
 //
 // Angles: the product of position and frequency in 64 bits, reduced there to
-// a fraction of a turn, so that far positions lose nothing; the rounding of
-// that fraction to 32 bits is given back to first order.
+// a fraction of a turn, so that far positions lose little (at 10^9 less than
+// 4e-7 of a radian); the rounding of that fraction to 32 bits is given back to
+// first order.
 #pragma once
 
 #include "kla_mixer.h"

@@ -51,6 +51,7 @@ def test_rotary_argument_errors(lib):
     assert f(*args(B=1 << 40, T=1 << 40)) == 1
     assert f(*args(H=1 << 32)) == 1
     assert f(*args(H=1 << 27)) == 1             # H * D = 2^31
+    assert f(*args(H=(1 << 25) + 1)) == 1       # H * D = 2^29 + 16
     for empty in ("B", "T", "H", "D"):
         assert f(*args(**{empty: 0}, x=None, out=None, rot=0)) == 0
 
