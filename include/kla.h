@@ -633,7 +633,9 @@ kla_status_t kla_rotary_forward(const void *x, const int64_t *x_strides, kla_dty
  *   q_out, k_out     dense, dtype (rounded once)
  *
  * The k and q of kla_layer_forward / kla_layer_step are such rows with D = Ns.
- * Sums and statistics are fp32.
+ * Sums and statistics are fp32: the sum of squares of a row has to stay below
+ * 2^127 (the row comes out as zeros where it overflows), and with eps 0 above
+ * 2^-100.
  */
 kla_status_t kla_qk_norm_rotary_forward(const void *q, const int64_t *q_strides, const void *k,
                                         const int64_t *k_strides, kla_dtype_t dtype, const float *q_weight,

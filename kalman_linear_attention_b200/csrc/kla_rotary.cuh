@@ -437,7 +437,7 @@ kla_rotary_kernel(const RotaryParams prm, const int table_pairs) {
                     if (live && two[u]) store_lane<VEC>(py + unit[u].b, vb[u]);
                 }
             } else {
-                // with p = g' x:  dw += r p,  dx = r (w g' - x r^2 mean(w p))
+                // with p = g' x:  dw += r p,  dx = r (w g' - x (r mean(w p)) r)
                 float2 dot = both(0.f);
                 const float2 rl = both(live ? r : 0.f);
 #pragma unroll
@@ -452,14 +452,16 @@ kla_rotary_kernel(const RotaryParams prm, const int table_pairs) {
                     }
                 }
                 if (x.y) {
+                    // r m is as large as w g', r as 1 / x: neither r^2 nor r^3,
+                    // out of fp32's range for rows of 1e15, stands alone
                     const float m = row_sum(dot.x + dot.y, lanes) * inv_d;
-                    const float2 k = both(-r * r * r * m), rr = both(r);
+                    const float2 k = both(-(r * m) * r), rr = both(r);
 #pragma unroll
                     for (int u = 0; u < UPL; ++u) {
 #pragma unroll
                         for (int j = 0; j < N; ++j) {
-                            ua[u].v[j] = __ffma2_rn(va[u].v[j], k, __fmul2_rn(rr, __fmul2_rn(wa[u].v[j], ua[u].v[j])));
-                            ub[u].v[j] = __ffma2_rn(vb[u].v[j], k, __fmul2_rn(rr, __fmul2_rn(wb[u].v[j], ub[u].v[j])));
+                            ua[u].v[j] = __fmul2_rn(rr, __ffma2_rn(va[u].v[j], k, __fmul2_rn(wa[u].v[j], ua[u].v[j])));
+                            ub[u].v[j] = __fmul2_rn(rr, __ffma2_rn(vb[u].v[j], k, __fmul2_rn(wb[u].v[j], ub[u].v[j])));
                         }
                         if (live && on[u]) store_lane<VEC>(py + unit[u].a, ua[u]);
                         if (live && two[u]) store_lane<VEC>(py + unit[u].b, ub[u]);

@@ -355,3 +355,44 @@ def test_offsets_past_32_bits():
     gq, _, _, _ = kla.qk_norm_rotary_backward(q, k, y, None, w, w, freq)
     tail = kla.qk_norm_rotary_backward(q[:, -9:], k[:, -9:], y[:, -9:], None, w, w, freq, position0=T - 9)
     assert torch.equal(gq[:, -9:], tail[0])
+
+
+@pytest.mark.parametrize("size,eps", [(1e13, 1e-6), (1e15, 1e-6), (1e17, 1e-6), (1e-13, 0.0), (1e-15, 0.0),
+                                      (1e-15, 1e-30)])
+@pytest.mark.parametrize("shape", [(2, 13, 3, 2, 64, 48), (1, 7, 2, 1, 250, 0), (1, 5, 2, 1, 7, 4)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_rows_far_from_one(shape, dtype, size, eps):
+    """Rows whose norm's cube is out of the range of fp32, the norm and all
+    that follows from it within.  The bounds are those of rows of any size: no
+    step of theirs rounds to a multiple of the smallest numbers."""
+    kla = _kla()
+    rot = shape[5]
+    x = make(shape, dtype, seed=12)
+    for name in ("q", "k"):
+        x[name] = (x[name].float() * size).to(dtype)
+    d = dev(x)
+    freq = frequencies(rot)
+    angle = angles(x["positions"], freq)
+    rotation = dict(inv_freq=None if freq is None else freq.to(DEV), positions=d["positions"], eps=eps)
+    got = kla.qk_norm_rotary_forward(d["q"], d["k"], d["wq"], d["wk"], **rotation)
+    grads = kla.qk_norm_rotary_backward(d["q"], d["k"], d["gq"], d["gk"], d["wq"], d["wk"], **rotation)
+    for name, y, gx, gw in (("q", got[0], grads[0], grads[2]), ("k", got[1], grads[1], grads[3])):
+        at = (double(x["w" + name]), eps, angle, rot, False, 1.0)
+        assert_within(y, *rounded(*reference(double(x[name]), *at), dtype), name)
+        dx, edx, dw, edw = reference_backward(double(x[name]), double(x["g" + name]), *at)
+        assert_within(gx, *rounded(dx, edx, dtype), "gradient of " + name)
+        assert_within(gw, dw, edw, "gradient of the weight of " + name)
+
+
+@pytest.mark.parametrize("eps", [1e-30, 1e-24, 1e-6])
+def test_gradients_of_rows_of_zeros(eps):
+    """A row of zeros passes its gradient on, divided by sqrt(eps)."""
+    kla = _kla()
+    g = torch.randn(2, 3, 2, 40, device=DEV)
+    q, k = torch.zeros_like(g), torch.zeros(2, 3, 1, 40, device=DEV)
+    gq, gk, gw, _ = kla.qk_norm_rotary_backward(q, k, g, g[:, :, :1].contiguous(), torch.ones(40, device=DEV), eps=eps)
+    # eps as the kernel has it; rsqrt's 4 u and two products
+    want = g.double() / np.sqrt(float(np.float32(eps)))
+    assert ((gq.double() - want).abs() <= 6 * U * want.abs()).all()
+    assert torch.equal(gk, gq[:, :, :1]) and not gw.any()
