@@ -573,8 +573,9 @@ kla_status_t kla_gated_scan_backward_workspace_size(int64_t B, int64_t T, int64_
  *              own.
  *
  * fp32 arithmetic; grad_f and grad_x are rounded once, on store.  B*H*N == 0
- * is a valid empty problem; T == 0 writes a zero grad_h0.  Outputs must not
- * overlap inputs, the workspace or each other.
+ * is a valid empty problem (N == 0 writes a zero grad_f for KLA_GATE_HEAD); T ==
+ * 0 writes a zero grad_h0.  Outputs must not overlap inputs, the workspace or
+ * each other.
  */
 kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype, kla_gate_t gate, const float *h0,
                                      const float *h, const float *g_h, void *grad_f, void *grad_x,

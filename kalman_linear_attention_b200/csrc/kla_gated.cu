@@ -356,8 +356,9 @@ KLA_API kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype
     if (ws != KLA_OK) return ws;
     Sizes s;
     sizes(B, T, H, N, gate, &s);
-    if (s.C == 0 || (!grad_f && !grad_x && !grad_h0)) return KLA_OK;
-    if (T > 0 && (!f || !g_h || (grad_f && !h))) return KLA_ERR_INVALID_ARG;
+    const bool unused = s.C == 0 && s.gates > 0 && grad_f;  // gates of heads without channels
+    if ((s.C == 0 && !unused) || (!grad_f && !grad_x && !grad_h0)) return KLA_OK;
+    if (s.n > 0 && (!f || !g_h || (grad_f && !h))) return KLA_ERR_INVALID_ARG;
     const int64_t e = dtype_size(in_dtype);
     const Range outs[4] = {range_of(grad_f, e * s.gates), range_of(grad_x, e * s.n), range_of(grad_h0, 4 * s.C),
                            range_of(workspace, (int64_t)workspace_bytes)};
@@ -369,6 +370,8 @@ KLA_API kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype
         if (!aligned(workspace, 256)) return KLA_ERR_MISALIGNED;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (unused)  // no state depends on them
+        return cudaMemsetAsync(grad_f, 0, (size_t)(e * s.gates), st) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
     if (T == 0) {  // no token: the loss does not depend on the entering state
         if (!grad_h0) return KLA_OK;
         return cudaMemsetAsync(grad_h0, 0, (size_t)(4 * s.C), st) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;

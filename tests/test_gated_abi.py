@@ -134,3 +134,14 @@ def test_reference_gradient_against_differences():
                 down = (reference(f, x, h0)[0] * g).sum()
                 a[at] = kept
                 assert abs((up - down) / 2e-6 - want[name][0][at]) < 1e-7, (name, at)
+
+
+def test_backward_of_heads_without_channels(lib):
+    """N = 0 with shared gates: the one gradient that has elements may not be
+    an input either; with none wanted, or a gate per channel, nothing is done."""
+    bwd = lib.kla_gated_scan_backward
+    args = lambda gate, gf, N=0: [P, 0, gate, None, None, None, gf, None, None, 1, 8, 2, N, None, 0, None]
+    assert bwd(*args(1, P + 4)) == 1
+    assert bwd(*args(1, None)) == 0
+    assert bwd(*args(0, 2 * P)) == 0
+    assert bwd(*args(1, 2 * P, N=4)) == 1        # channels, and no states or gradients given

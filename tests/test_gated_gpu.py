@@ -447,3 +447,19 @@ def test_a_step_on_saved_states_is_noticed():
     with torch.inference_mode():  # tensors without versions
         state = torch.zeros(1, 2, 8, device="cuda")
         assert kla.gated_scan_step(x[:, 0].contiguous(), x[:, 1].contiguous(), state) is state
+
+
+def test_heads_without_channels():
+    """The gradient of a gate that no channel has used is zero."""
+    kla = _kla()
+    f = torch.rand(2, 50, 3, device=DEV)
+    for dtype in (torch.float32, torch.bfloat16):
+        x = torch.empty(2, 50, 3, 0, device=DEV, dtype=dtype)
+        h = torch.empty(2, 50, 3, 0, device=DEV)
+        # blocks that the allocator hands out next hold NaN
+        torch.cuda.synchronize()
+        held = [torch.full(f.shape, float("nan"), device=DEV, dtype=dtype) for _ in range(8)]
+        del held
+        gf, gx, gh0 = kla.gated_scan_backward(f.to(dtype), h, h)
+        assert gf.shape == f.shape and not gf.any()
+        assert gx.shape == x.shape and gh0.shape == (2, 3, 0)
