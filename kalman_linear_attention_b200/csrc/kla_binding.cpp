@@ -5,7 +5,9 @@
 // four microseconds; marshalling it in Python took six to seventeen.
 //
 // Work goes to `stream` (None: the current stream of the tensors' device), and
-// what a call allocates belongs to that stream, whichever one is current.
+// what a call allocates belongs to that stream, whichever one is current.  Other
+// Python threads run while it allocates and launches: an allocation may wait for
+// the device, a launch waits where the stream's queue is full.
 #include "kla.h"
 
 #include <ATen/ATen.h>
@@ -46,6 +48,12 @@ std::string dtype_name(at::ScalarType t) {
     Py_XDECREF(o);
     return s;
 }
+
+// Python's lock, let go of while this lives.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 const Tensor &tensor(PyObject *o, const char *name) {
     if (!THPVariable_Check(o)) refuse(PyExc_TypeError, text(name, " must be a tensor"));
@@ -117,6 +125,17 @@ void check(kla_status_t status, const char *name) {
     throw Refused();
 }
 
+// The part of a call that allocates and launches, without Python's lock.
+template <typename F>
+void enqueue(const char *name, F part) {
+    kla_status_t status;
+    {
+        const Unlocked others;
+        status = part();
+    }
+    check(status, name);
+}
+
 kla_dtype_t code_of(const Tensor &t) {
     if (t.scalar_type() == at::kFloat) return KLA_F32;
     if (t.scalar_type() == at::kBFloat16) return KLA_BF16;
@@ -174,21 +193,23 @@ PyObject *given_or(PyObject *o, const Tensor &t) {
 }
 void *address(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 
-// A caller's workspace, or a new one of `bytes` bytes.
+// A caller's workspace, or a new one.
 struct Workspace {
     Tensor own;
     void *p = nullptr;
     size_t bytes = 0;
-    Workspace(const Place &at, PyObject *given, size_t need) {
-        if (given != Py_None) {
-            const Tensor &t = tensor(given, "workspace");
-            p = at.dense("workspace", t, t.sizes(), t.scalar_type());
-            bytes = t.nbytes();
-        } else if (need > 0) {
-            own = at.empty({(int64_t)need}, at::kByte);
-            p = own.data_ptr();
-            bytes = need;
-        }
+    Workspace(const Place &at, PyObject *given) {
+        if (given == Py_None) return;
+        const Tensor &t = tensor(given, "workspace");
+        p = at.dense("workspace", t, t.sizes(), t.scalar_type());
+        bytes = t.nbytes();
+    }
+    // A new one of `need` bytes (0: none, or there is a given one).
+    void have(const Place &at, size_t need) {
+        if (need == 0) return;
+        own = at.empty({(int64_t)need}, at::kByte);
+        p = own.data_ptr();
+        bytes = need;
     }
 };
 
@@ -207,12 +228,14 @@ PyObject *gated_scan_forward(PyObject *const *a) {
     void *ph = at.maybe("out", a[3], s, at::kFloat);
     const Enqueue on(at, a[4]);
     Tensor h;
-    if (a[3] == Py_None) {
-        h = at.empty(s, at::kFloat);
-        ph = h.data_ptr();
-    }
-    check(kla_gated_scan_forward(pf, px, code, gate, static_cast<const float *>(h0), static_cast<float *>(ph), s[0], s[1],
-                                 s[2], s[3], on.handle), "kla_gated_scan_forward");
+    enqueue("kla_gated_scan_forward", [&] {
+        if (a[3] == Py_None) {
+            h = at.empty(s, at::kFloat);
+            ph = h.data_ptr();
+        }
+        return kla_gated_scan_forward(pf, px, code, gate, static_cast<const float *>(h0), static_cast<float *>(ph), s[0],
+                                      s[1], s[2], s[3], on.handle);
+    });
     return given_or(a[3], h);
 }
 
@@ -230,8 +253,10 @@ PyObject *gated_scan_step(PyObject *const *a) {
     PyObject *out = a[3] == Py_None ? a[2] : a[3];
     void *ph = a[3] == Py_None ? h : at.dense("out", tensor(a[3], "out"), s, at::kFloat);
     const Enqueue on(at, a[4]);
-    check(kla_gated_scan_step(pf, px, code, gate, static_cast<const float *>(h), static_cast<float *>(ph), s[0], s[1], s[2],
-                              on.handle), "kla_gated_scan_step");
+    enqueue("kla_gated_scan_step", [&] {
+        return kla_gated_scan_step(pf, px, code, gate, static_cast<const float *>(h), static_cast<float *>(ph), s[0], s[1],
+                                   s[2], on.handle);
+    });
     return given_or(out, Tensor());
 }
 
@@ -252,15 +277,18 @@ PyObject *gated_scan_backward(PyObject *const *a) {
         check(kla_gated_scan_backward_workspace_size(s[0], s[1], s[2], s[3], code, gate, &need),
               "kla_gated_scan_backward_workspace_size");
     const Enqueue on(at, a[8]);
-    const Workspace room(at, a[7], need);
+    Workspace room(at, a[7]);
     Tensor gf, gx, gh0;
-    if (want[0]) gf = at.empty(f.sizes(), f.scalar_type());
-    if (want[1]) gx = at.empty(s, f.scalar_type());
-    if (want[2]) gh0 = at.empty({s[0], s[2], s[3]}, at::kFloat);
-    check(kla_gated_scan_backward(pf, code, gate, static_cast<const float *>(h0), static_cast<const float *>(ph),
-                                  static_cast<const float *>(pg), address(gf), address(gx),
-                                  static_cast<float *>(address(gh0)), s[0], s[1], s[2], s[3], room.p, room.bytes,
-                                  on.handle), "kla_gated_scan_backward");
+    enqueue("kla_gated_scan_backward", [&] {
+        room.have(at, need);
+        if (want[0]) gf = at.empty(f.sizes(), f.scalar_type());
+        if (want[1]) gx = at.empty(s, f.scalar_type());
+        if (want[2]) gh0 = at.empty({s[0], s[2], s[3]}, at::kFloat);
+        return kla_gated_scan_backward(pf, code, gate, static_cast<const float *>(h0), static_cast<const float *>(ph),
+                                       static_cast<const float *>(pg), address(gf), address(gx),
+                                       static_cast<float *>(address(gh0)), s[0], s[1], s[2], s[3], room.p, room.bytes,
+                                       on.handle);
+    });
     return tuple(gf, gx, gh0);
 }
 
@@ -312,15 +340,19 @@ PyObject *rotary_forward(PyObject *const *a) {
     const Place at(x);
     const Rotation r(at, s[0], s[1], s[3], a[1], a[2]);
     void *py = at.maybe("out", a[7], s, x.scalar_type());
+    const int64_t position0 = integer(a[3]);
+    const bool interleaved = truth(a[4]), inverse = truth(a[6]);
+    const float scale = real(a[5]);
     const Enqueue on(at, a[8]);
     Tensor y;
-    if (a[7] == Py_None) {
-        y = at.empty(s, x.scalar_type());
-        py = y.data_ptr();
-    }
-    check(kla_rotary_forward(x.data_ptr(), strides.data(), code, r.freq, r.rot, truth(a[4]), real(a[5]), truth(a[6]),
-                             r.positions, r.stride, integer(a[3]), py, s[0], s[1], s[2], s[3], on.handle),
-          "kla_rotary_forward");
+    enqueue("kla_rotary_forward", [&] {
+        if (a[7] == Py_None) {
+            y = at.empty(s, x.scalar_type());
+            py = y.data_ptr();
+        }
+        return kla_rotary_forward(x.data_ptr(), strides.data(), code, r.freq, r.rot, interleaved, scale, inverse,
+                                  r.positions, r.stride, position0, py, s[0], s[1], s[2], s[3], on.handle);
+    });
     return given_or(a[7], y);
 }
 
@@ -363,18 +395,20 @@ PyObject *qk_norm_rotary_forward(PyObject *const *a) {
     void *pq = c.at.maybe("out", a[10], c.q.sizes(), type), *pk = c.at.maybe("out", a[11], c.k.sizes(), type);
     const Enqueue on(c.at, a[12]);
     Tensor yq, yk;
-    if (a[10] == Py_None) {
-        yq = c.at.empty(c.q.sizes(), type);
-        pq = yq.data_ptr();
-    }
-    if (a[11] == Py_None) {
-        yk = c.at.empty(c.k.sizes(), type);
-        pk = yk.data_ptr();
-    }
-    check(kla_qk_norm_rotary_forward(c.q.data_ptr(), c.qs.data(), c.k.data_ptr(), c.ks.data(), c.code, c.qw, c.kw, c.eps,
-                                     c.r.freq, c.r.rot, c.interleaved, c.scale, c.r.positions, c.r.stride, c.position0, pq,
-                                     pk, c.q.size(0), c.q.size(1), c.q.size(2), c.k.size(2), c.q.size(3), on.handle),
-          "kla_qk_norm_rotary_forward");
+    enqueue("kla_qk_norm_rotary_forward", [&] {
+        if (a[10] == Py_None) {
+            yq = c.at.empty(c.q.sizes(), type);
+            pq = yq.data_ptr();
+        }
+        if (a[11] == Py_None) {
+            yk = c.at.empty(c.k.sizes(), type);
+            pk = yk.data_ptr();
+        }
+        return kla_qk_norm_rotary_forward(c.q.data_ptr(), c.qs.data(), c.k.data_ptr(), c.ks.data(), c.code, c.qw, c.kw,
+                                          c.eps, c.r.freq, c.r.rot, c.interleaved, c.scale, c.r.positions, c.r.stride,
+                                          c.position0, pq, pk, c.q.size(0), c.q.size(1), c.q.size(2), c.k.size(2),
+                                          c.q.size(3), on.handle);
+    });
     PyObject *o = PyTuple_New(2);
     if (!o) throw Refused();
     PyTuple_SET_ITEM(o, 0, given_or(a[10], yq));
@@ -396,17 +430,21 @@ PyObject *qk_norm_rotary_backward(PyObject *const *a) {
         check(kla_qk_norm_rotary_backward_workspace_size(c.q.size(2), c.k.size(2), D, &need),
               "kla_qk_norm_rotary_backward_workspace_size");
     const Enqueue on(c.at, a[17]);
-    const Workspace room(c.at, a[16], need);
+    Workspace room(c.at, a[16]);
     Tensor dq, dk, dqw, dkw;
-    if (want[0]) dq = c.at.empty(c.q.sizes(), type);
-    if (want[1]) dk = c.at.empty(c.k.sizes(), type);
-    if (want[2]) dqw = c.at.empty({D}, at::kFloat);
-    if (want[3]) dkw = c.at.empty({D}, at::kFloat);
-    check(kla_qk_norm_rotary_backward(c.q.data_ptr(), c.qs.data(), c.k.data_ptr(), c.ks.data(), c.code, c.qw, c.kw, c.eps,
-                                      c.r.freq, c.r.rot, c.interleaved, c.scale, c.r.positions, c.r.stride, c.position0, gq,
-                                      gk, address(dq), address(dk), static_cast<float *>(address(dqw)),
-                                      static_cast<float *>(address(dkw)), c.q.size(0), c.q.size(1), c.q.size(2),
-                                      c.k.size(2), D, room.p, room.bytes, on.handle), "kla_qk_norm_rotary_backward");
+    enqueue("kla_qk_norm_rotary_backward", [&] {
+        room.have(c.at, need);
+        if (want[0]) dq = c.at.empty(c.q.sizes(), type);
+        if (want[1]) dk = c.at.empty(c.k.sizes(), type);
+        if (want[2]) dqw = c.at.empty({D}, at::kFloat);
+        if (want[3]) dkw = c.at.empty({D}, at::kFloat);
+        return kla_qk_norm_rotary_backward(c.q.data_ptr(), c.qs.data(), c.k.data_ptr(), c.ks.data(), c.code, c.qw, c.kw,
+                                           c.eps, c.r.freq, c.r.rot, c.interleaved, c.scale, c.r.positions, c.r.stride,
+                                           c.position0, gq, gk, address(dq), address(dk),
+                                           static_cast<float *>(address(dqw)), static_cast<float *>(address(dkw)),
+                                           c.q.size(0), c.q.size(1), c.q.size(2), c.k.size(2), D, room.p, room.bytes,
+                                           on.handle);
+    });
     return tuple(dq, dk, dqw, dkw);
 }
 
