@@ -647,7 +647,8 @@ kla_status_t kla_qk_norm_rotary_forward(const void *q, const int64_t *q_strides,
 
 /*
  * Device workspace that kla_qk_norm_rotary_backward needs when a weight's
- * gradient is wanted (one row of sums per CTA), written to *bytes.
+ * gradient is wanted (one row of sums per CTA of the current device, which has
+ * to be the tensors'), written to *bytes.
  */
 kla_status_t kla_qk_norm_rotary_backward_workspace_size(int64_t Hq, int64_t Hk, int64_t D, size_t *bytes);
 

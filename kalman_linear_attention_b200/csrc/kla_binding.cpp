@@ -425,11 +425,11 @@ PyObject *qk_norm_rotary_backward(PyObject *const *a) {
     const bool want[4] = {truth(a[12]) && has_q, truth(a[13]) && has_k, truth(a[14]) && has_q && c.qw,
                           truth(a[15]) && has_k && c.kw};
     const int64_t D = c.q.size(3);
-    size_t need = 0;
+    const Enqueue on(c.at, a[17]);
+    size_t need = 0;  // it depends on the current device
     if ((want[2] || want[3]) && a[16] == Py_None)
         check(kla_qk_norm_rotary_backward_workspace_size(c.q.size(2), c.k.size(2), D, &need),
               "kla_qk_norm_rotary_backward_workspace_size");
-    const Enqueue on(c.at, a[17]);
     Workspace room(c.at, a[16]);
     Tensor dq, dk, dqw, dkw;
     enqueue("kla_qk_norm_rotary_backward", [&] {

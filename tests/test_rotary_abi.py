@@ -173,3 +173,12 @@ def test_reference_gradients_against_differences(interleaved):
             down = (reference(x, w, *at)[0] * g).sum()
             flat[i] = kept
             assert abs((up - down) / 2e-6 - want[i]) < 1e-7
+
+
+def test_backward_workspace_is_asked_for_on_the_tensors_device():
+    """The size depends on the current device: nothing is asked before the
+    tensors' device is known to be one (a row that is too long shows it)."""
+    import kalman_linear_attention_b200 as kla
+    x, w = torch.rand(1, 2, 1, 1026), torch.ones(1026)
+    with pytest.raises(ValueError, match="CUDA"):
+        kla.qk_norm_rotary_backward(x, x, x, x, w, w)
