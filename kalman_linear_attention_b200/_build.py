@@ -5,7 +5,9 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
+from importlib import metadata
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -42,7 +44,7 @@ def up_to_date() -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Build libkla.so and _mixer.so next to this file (each a no-op when it is
-    newer than its sources)."""
+    newer than its sources, and _mixer.so for this torch and Python)."""
     build_library(force, verbose)
     build_binding(force)
     return LIBRARY
@@ -60,11 +62,29 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     return LIBRARY
 
 
+def built_for() -> str:
+    """The torch and Python that _mixer.so is for; what it was built for stands in it."""
+    try:
+        torch_version = metadata.version("torch")
+    except metadata.PackageNotFoundError:  # torch from a source tree
+        import torch
+        torch_version = torch.__version__
+    return f"torch {torch_version}, Python {sys.version_info.major}.{sys.version_info.minor}"
+
+
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    if not all(os.path.getmtime(f) <= t for f in (BINDING_SOURCE, os.path.join(INCLUDE, "kla.h"))):
+        return False
+    with open(BINDING, "rb") as f:
+        return b"\0" + built_for().encode() + b"\0" in f.read()
+
+
 def build_binding(force: bool = False) -> str:
     """_mixer.so, linked to torch's libraries and to libkla.so beside it."""
-    depends = [BINDING_SOURCE, os.path.join(INCLUDE, "kla.h")]
-    if not force and os.path.exists(BINDING) and all(
-            os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in depends):
+    if not force and binding_up_to_date():
         return BINDING
     import torch
     from torch.utils import cpp_extension
@@ -73,7 +93,7 @@ def build_binding(force: bool = False) -> str:
     includes = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_paths()["include"], cuda]
     libraries = [p for p in cpp_extension.library_paths() if os.path.isdir(p)]
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", BINDING_SOURCE,
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DKLA_BUILT_FOR="{built_for()}"',
            *[f"-isystem{p}" for p in includes], "-o", tmp, *[f"-L{p}" for p in libraries], f"-L{HERE}",
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-l:libkla.so", "-Wl,-rpath,$ORIGIN"]
     subprocess.run(cmd, check=True)

@@ -666,15 +666,21 @@ _mixer = None
 
 
 def _native():
-    """The extension ``_mixer.so`` (raises if it is missing)."""
+    """The extension ``_mixer.so`` (raises if it is missing, or for another torch or Python)."""
     global _mixer
     if _mixer is None:
         lib()  # raises if libkla.so, which it is linked to, is missing
+        from . import _build
+        build = "build it with `python -m kalman_linear_attention_b200._build`"
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"the binding of the mixer operators is not built; {build}")
         try:
             from . import _mixer as module
         except ImportError as e:
-            raise RuntimeError("the binding of the mixer operators is not built; build it with "
-                               "`python -m kalman_linear_attention_b200._build`") from e
+            raise RuntimeError(f"the binding of the mixer operators could not be loaded ({e}); {build}") from e
+        if module.built_for != _build.built_for():
+            raise RuntimeError(f"the binding of the mixer operators is for {module.built_for}, "
+                               f"this is {_build.built_for()}; {build}")
         module.set_error(KlaError)
         _mixer = module
     return _mixer

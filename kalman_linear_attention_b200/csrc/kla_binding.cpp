@@ -486,6 +486,17 @@ PyMethodDef methods[] = {
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mixer", "Binding of the mixer operators.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
+// The torch and Python that this was built for, between zeros: found by the
+// build without loading it.
+const char g_built_for[] = "\0" KLA_BUILT_FOR;
+
 }  // namespace
 
-PyMODINIT_FUNC PyInit__mixer() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__mixer() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", g_built_for + 1) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
