@@ -314,7 +314,8 @@ struct Rows {
     static __device__ __forceinline__ int shift(int64_t first, int64_t step, int i) {
         if constexpr (COPY != SHIFT) return 0;
         constexpr int E = 16 / (int)sizeof(T);
-        return (((int)first + i * (int)step) & (E - 1)) * (int)sizeof(T);
+        // the low bits alone: offsets past 32 bits wrap
+        return (int)(((unsigned)first + (unsigned)i * (unsigned)step) & (unsigned)(E - 1)) * (int)sizeof(T);
     }
 };
 

@@ -463,3 +463,27 @@ def test_heads_without_channels():
         gf, gx, gh0 = kla.gated_scan_backward(f.to(dtype), h, h)
         assert gf.shape == f.shape and not gf.any()
         assert gx.shape == x.shape and gh0.shape == (2, 3, 0)
+
+
+@pytest.mark.parametrize("gate", ["channel", "head"])
+def test_offsets_past_32_bits_of_rows_off_16_bytes(gate):
+    """2^31 elements lie two tokens before the end of rows that start anywhere."""
+    kla = _kla()
+    B, T, H, N = shape = (1, 33001, 1, 65077)
+    assert 0 < B * T * H * N - 2 ** 31 < 2 * H * N and H * N * 2 % 16
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    f = torch.rand(shape if gate == "channel" else shape[:3], generator=gen, device=DEV, dtype=torch.bfloat16)
+    x = torch.randn(shape, generator=gen, device=DEV, dtype=torch.bfloat16)
+    h = kla.gated_scan_forward(f, x)
+    # as above: 150 tokens after a state of unknown error nothing is left of it
+    k = 150
+    late = np.s_[:, -k - 40:]
+    ref, err = reference(_np(f[late]), _np(x[late]), _np(h[:, -k - 41]))
+    assert np.prod(_np(f[:, -k - 40:-40]), axis=1).max() < 1e-30
+    assert_within(h[:, -40:], ref[:, -40:], err[:, -40:], "last tokens")
+    del x
+    gf, gx, _ = kla.gated_scan_backward(f, h, h)
+    sl = np.s_[:, -40:]
+    want = reference_backward(_np(f[sl]), _np(h[sl]), _np(h[sl]), _np(h[:, -41]), HALF_STEP[torch.bfloat16])
+    assert_within(gx[sl], *want["x"], "last gradients of x")
+    assert_within(gf[sl], *want["f"], "last gradients of f")
