@@ -808,8 +808,16 @@ def rotary_forward(x: torch.Tensor, inv_freq: torch.Tensor, positions: Optional[
                                                 stream)
 
 
+def _not_formed(ctx, first, *names):
+    """Refuse a backward pass that wants the gradient of an input from ``first`` on."""
+    for name, wanted in zip(names, ctx.needs_input_grad[first:]):
+        if wanted:
+            raise RuntimeError(f"the gradient of {name} is not formed; pass it without requires_grad")
+
+
 class Rotary(torch.autograd.Function):
-    """Differentiable rotary_forward: the gradient is the inverse rotation."""
+    """Differentiable rotary_forward: the gradient is the inverse rotation.
+    Frequencies that want a gradient are refused in the backward pass."""
 
     @staticmethod
     def forward(ctx, x, inv_freq, positions, position0, interleaved, scale):
@@ -820,6 +828,7 @@ class Rotary(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, g):
+        _not_formed(ctx, 1, "inv_freq", "positions", "position0", "interleaved", "scale")
         inv_freq, positions = ctx.saved_tensors
         return (rotary_forward(g.contiguous(), inv_freq, positions, inverse=True, **ctx.rotation),
                 None, None, None, None, None)
@@ -827,7 +836,7 @@ class Rotary(torch.autograd.Function):
 
 def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions: Optional[torch.Tensor] = None, *,
            position0: int = 0, interleaved: bool = False, scale: float = 1.0) -> torch.Tensor:
-    """rotary_forward, differentiable with respect to x."""
+    """rotary_forward, differentiable with respect to x alone."""
     return Rotary.apply(x, inv_freq, positions, position0, interleaved, scale)
 
 
@@ -874,7 +883,8 @@ def qk_norm_rotary_backward(q: torch.Tensor, k: torch.Tensor, g_q: Optional[torc
 
 class QKNormRotary(torch.autograd.Function):
     """Differentiable QK-Norm with rotation: forward =
-    kla_qk_norm_rotary_forward, backward = kla_qk_norm_rotary_backward."""
+    kla_qk_norm_rotary_forward, backward = kla_qk_norm_rotary_backward.
+    Frequencies that want a gradient are refused in the backward pass."""
 
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, inv_freq, positions, position0, eps, interleaved, scale):
@@ -886,6 +896,7 @@ class QKNormRotary(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, g_q, g_k):
+        _not_formed(ctx, 4, "inv_freq", "positions", "position0", "eps", "interleaved", "scale")
         q, k, *rest = ctx.saved_tensors
         grads = [None if g is None else g.contiguous() for g in (g_q, g_k)]
         got = qk_norm_rotary_backward(q, k, *grads, *rest, **ctx.options, want=ctx.needs_input_grad[:4])
@@ -897,5 +908,5 @@ def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Te
                    positions: Optional[torch.Tensor] = None, *, position0: int = 0, eps: float = 1e-6,
                    interleaved: bool = False, scale: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
     """qk_norm_rotary_forward, differentiable with respect to q, k and the
-    weights."""
+    weights alone."""
     return QKNormRotary.apply(q, k, q_weight, k_weight, inv_freq, positions, position0, eps, interleaved, scale)

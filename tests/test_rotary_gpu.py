@@ -396,3 +396,21 @@ def test_gradients_of_rows_of_zeros(eps):
     want = g.double() / np.sqrt(float(np.float32(eps)))
     assert ((gq.double() - want).abs() <= 6 * U * want.abs()).all()
     assert torch.equal(gk, gq[:, :, :1]) and not gw.any()
+
+
+@pytest.mark.parametrize("name", ["inv_freq", "scale", "eps"])
+def test_gradients_that_are_not_formed_are_refused(name):
+    """Learned frequencies do not go without a gradient unnoticed."""
+    kla = _kla()
+    x = torch.rand(1, 2, 1, 8, device=DEV, requires_grad=True)
+    learned = {"inv_freq": frequencies(8).to(DEV).requires_grad_(), "scale": torch.ones((), requires_grad=True),
+               "eps": torch.full((), 1e-6, requires_grad=True)}[name]
+    options = {"inv_freq": frequencies(8).to(DEV), name: learned}
+    calls = [lambda: kla.qk_norm_rotary(x, x, **options)[1]]
+    if name != "eps":
+        calls.append(lambda: kla.rotary(x, **options))
+    for call in calls:
+        with pytest.raises(RuntimeError, match=f"gradient of {name}"):
+            call().sum().backward()
+        with torch.no_grad():  # none is wanted
+            assert call().shape == x.shape
