@@ -91,6 +91,18 @@ typedef enum {
     KLA_GATE_HEAD = 1     /* one gate per head, shared by its N channels: f is [B, T, H] */
 } kla_gate_t;
 
+/* How kla_gated_scan_forward or kla_gated_scan_backward runs. */
+typedef struct {
+    int64_t tiles;  /* of `channels` channels of one batch row; a CTA or a cluster for each */
+    int64_t rounds; /* of cluster * warps * parts * tokens tokens, in which it walks the sequence */
+    int channels;   /* of a tile */
+    int parts;      /* that a warp's lanes are in, each with tokens of its own */
+    int tokens;     /* of a lane in a round */
+    int warps;      /* of a CTA */
+    int cluster;    /* CTAs that share a tile */
+    int whole_rows; /* 1: all rows start on 16 bytes and are copied as they are, two channels a lane; 0: they do not */
+} kla_gated_plan_t;
+
 /* ABI version of the loaded library (KLA_ABI_VERSION it was built with). */
 int kla_abi_version(void);
 
@@ -532,6 +544,14 @@ kla_status_t kla_scan_forward_lti_plan(int64_t B, int64_t T, int64_t H, int64_t 
 kla_status_t kla_gated_scan_forward(const void *f, const void *x, kla_dtype_t in_dtype, kla_gate_t gate,
                                     const float *h0, float *h, int64_t B, int64_t T, int64_t H, int64_t N,
                                     void *stream);
+
+/*
+ * How kla_gated_scan_forward (backward 0), or kla_gated_scan_backward with
+ * grad_f wanted (backward 1), runs on the current device for arrays that start
+ * on 16 bytes, written to *plan (all zero for an empty problem).
+ */
+kla_status_t kla_gated_scan_plan(int64_t B, int64_t T, int64_t H, int64_t N, kla_dtype_t in_dtype, kla_gate_t gate,
+                                 int backward, kla_gated_plan_t *plan);
 
 /*
  * One decode token of it: h_out = f h + x.

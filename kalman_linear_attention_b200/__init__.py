@@ -14,7 +14,7 @@ _API_NAMES = {
     "scan_backward", "backward_workspace_size", "backward_plan", "debug_force_backward_kernel",
     "KalmanFilterScan", "kalman_filter", "layer_forward", "layer_workspace_size", "layer_step",
     "attention_weights", "scan_forward_lti", "lti_workspace_size", "lti_plan",
-    "gated_scan_forward", "gated_scan_step", "gated_scan_backward", "gated_scan_backward_workspace_size",
+    "gated_scan_forward", "gated_scan_step", "gated_scan_backward", "gated_scan_backward_workspace_size", "gated_scan_plan",
     "GatedScan", "gated_scan",
     "rotary_frequencies", "rotary_forward", "Rotary", "rotary", "qk_norm_rotary_forward", "qk_norm_rotary_backward",
     "qk_norm_rotary_backward_workspace_size", "QKNormRotary", "qk_norm_rotary", "QKNorm",

@@ -78,6 +78,7 @@ SIGNATURES = {
                                                  ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
     "kla_gated_scan_forward": (ctypes.c_int, [_VP, _VP, ctypes.c_int, ctypes.c_int, _VP, _VP, _I64, _I64, _I64,
                                               _I64, _VP]),
+    "kla_gated_scan_plan": (ctypes.c_int, [_I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _VP]),
     "kla_gated_scan_step": (ctypes.c_int, [_VP, _VP, ctypes.c_int, ctypes.c_int, _VP, _VP, _I64, _I64, _I64, _VP]),
     "kla_gated_scan_backward_workspace_size": (ctypes.c_int, [_I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int,
                                                               ctypes.POINTER(_SZ)]),
@@ -696,6 +697,33 @@ def gated_scan_forward(f: torch.Tensor, x: torch.Tensor, h0: Optional[torch.Tens
     last one continues with gated_scan_step.  Enqueued on ``stream`` (default:
     the current stream) without synchronising."""
     return (_mixer or _native()).gated_scan_forward(f, x, h0, out, stream)
+
+
+class GatedPlan(NamedTuple):
+    """How a gated scan runs (kla_gated_plan_t)."""
+    tiles: int
+    rounds: int
+    channels: int
+    parts: int
+    tokens: int
+    warps: int
+    cluster: int
+    whole_rows: int
+
+
+class _GatedPlan(ctypes.Structure):
+    _fields_ = [("tiles", _I64), ("rounds", _I64)] + [(n, ctypes.c_int) for n in GatedPlan._fields[2:]]
+
+
+def gated_scan_plan(B: int, T: int, H: int, N: int, dtype: torch.dtype = torch.float32, head_gate: bool = False,
+                    backward: bool = False) -> GatedPlan:
+    """How gated_scan_forward, or gated_scan_backward, runs on aligned arrays of
+    these sizes (kla_gated_scan_plan)."""
+    code = KLA_BF16 if dtype == torch.bfloat16 else KLA_F32
+    out = _GatedPlan()
+    _check(lib().kla_gated_scan_plan(B, T, H, N, code, int(head_gate), int(backward), ctypes.byref(out)),
+           "kla_gated_scan_plan")
+    return GatedPlan(*(getattr(out, n) for n in GatedPlan._fields))
 
 
 def gated_scan_step(f: torch.Tensor, x: torch.Tensor, h_state: torch.Tensor, *,

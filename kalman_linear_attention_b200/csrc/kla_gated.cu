@@ -119,7 +119,7 @@ struct Resident {
 // 12 x 80, 21 us against 27), or 1.5 of them with one channel a lane.  Rows that start
 // on 16 bytes, and on pairs of channels in every array, take two channels a
 // lane (half the instructions for a channel, and two chains of multiply-adds
-// side by side), others one; a warp's lanes in 1, 2, 4 or 8 parts.
+// side by side), others one; a warp's lanes in 1, 2, 4 or (fp32) 8 parts.
 template <typename F>
 Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, const Array *arrays, int n, const F &resident) {
     Launch l;
@@ -137,10 +137,13 @@ Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, const Array *arrays, int
         k.copy = copy_of(HN, k.g.seg, arrays, n);
         if (vec == 2 ? !pairs || k.copy != WIDE : any) continue;
         if (vec == 1 && k.copy == WIDE) k.copy = SHIFT;
-        // parts no shorter than a sector of memory a row
+        // Parts whose rows are no shorter than a sector of memory in the inputs'
+        // type: bf16 in 4 parts at most (T=65536, 2 x 64, backward: shared gates
+        // 64 us, 86 with 8; a gate for each channel 78, 79; B=8, T=8192: 33, 41;
+        // forward 41 us, 39 with 8; 45, 47; 23, 27)
         k.few = k.tiles <= sms;
         const int64_t L = resident.tokens(k.few);
-        if (S > 1 && (k.copy == NARROW || (T + L - 1) / L < S || (vec == 2 && 64 / S * arrays[0].size < 32)))
+        if (S > 1 && (k.copy == NARROW || (T + L - 1) / L < S || (vec == 2 && 64 / S * dtype_size(resident.dt) < 32)))
             continue;
         l = k;
         any = any || vec == 2;
@@ -167,6 +170,24 @@ Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, const Array *arrays, int
     // that had to wait for others would run alone at the end)
     if (l.C == 1) l.W = (int)std::max<int64_t>(1, std::min<int64_t>(l.W, held / ((l.tiles + sms - 1) / sms)));
     return l;
+}
+
+// How a call runs.  A gate for each head of one channel is a gate for each
+// channel; the arrays of gates shared by a head are read element by element.
+Launch plan_forward(int64_t B, int64_t T, int64_t H, int64_t N, kla_dtype_t dt, kla_gate_t gate, const void *f,
+                    const void *x, const float *h) {
+    const bool head = gate == KLA_GATE_HEAD && N > 1;
+    const int64_t e = dtype_size(dt);
+    const Array arrays[3] = {{x, e, true}, {h, 4, false}, {f, e, true}};
+    return plan(B, T, H, N, arrays, head ? 2 : 3, Resident{dt, head, false});
+}
+Launch plan_backward(int64_t B, int64_t T, int64_t H, int64_t N, kla_dtype_t dt, kla_gate_t gate, const void *f,
+                     const float *h, const float *g_h, const void *grad_f, const void *grad_x) {
+    const bool head = gate == KLA_GATE_HEAD && N > 1;
+    const int64_t e = dtype_size(dt);
+    const Array arrays[5] = {{g_h, 4, true}, {grad_f ? h : nullptr, 4, true}, {grad_x, e, false},
+                             {f, e, true}, {grad_f, e, false}};
+    return plan(B, T, H, N, arrays, head ? 3 : 5, Resident{dt, head, true});
 }
 
 // Tiles (of cw channels) of a head whose gate gradients the reduce kernel adds up.
@@ -243,10 +264,11 @@ cudaError_t run_form(const Launch &l, const Params &prm, cudaStream_t st) {
         return l.S == 1   ? run_scan<Tin, 1, 1, HEAD, SHIFT>(l, prm, st)
                : l.S == 2 ? run_scan<Tin, 1, 2, HEAD, SHIFT>(l, prm, st)
                           : run_scan<Tin, 1, 4, HEAD, SHIFT>(l, prm, st);
+    if constexpr (sizeof(Tin) == 4)
+        if (l.S == 8) return run_scan<Tin, 2, 8, HEAD, WIDE>(l, prm, st);
     return l.S == 1   ? run_scan<Tin, 2, 1, HEAD, WIDE>(l, prm, st)
            : l.S == 2 ? run_scan<Tin, 2, 2, HEAD, WIDE>(l, prm, st)
-           : l.S == 4 ? run_scan<Tin, 2, 4, HEAD, WIDE>(l, prm, st)
-                      : run_scan<Tin, 2, 8, HEAD, WIDE>(l, prm, st);
+                      : run_scan<Tin, 2, 4, HEAD, WIDE>(l, prm, st);
 }
 template <typename Params>
 cudaError_t run_type(const Launch &l, kla_dtype_t dt, bool head, const Params &prm, cudaStream_t st) {
@@ -298,15 +320,37 @@ KLA_API kla_status_t kla_gated_scan_forward(const void *f, const void *x, kla_dt
     const Range ins[3] = {range_of(f, e * s.gates), range_of(x, e * s.n), range_of(h0, 4 * s.C)};
     if (any_overlap(outs, 1, ins, 3)) return KLA_ERR_INVALID_ARG;
 
-    // a gate for each head of one channel is a gate for each channel
     const bool head = gate == KLA_GATE_HEAD && N > 1;
-    const Array arrays[3] = {{x, e, true}, {h, 4, false}, {f, e, true}};
-    const Launch l = plan(B, T, H, N, arrays, head ? 2 : 3, Resident{in_dtype, head, false});
+    const Launch l = plan_forward(B, T, H, N, in_dtype, gate, f, x, h);
     if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
     GatedParams prm;
     prm.g = l.g;
     prm.f = f; prm.x = x; prm.h0 = h0; prm.h = h; prm.n = s.n;
     return run_type(l, in_dtype, head, prm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+KLA_API kla_status_t kla_gated_scan_plan(int64_t B, int64_t T, int64_t H, int64_t N, kla_dtype_t in_dtype,
+                                         kla_gate_t gate, int backward, kla_gated_plan_t *out) {
+    if (!out || B < 0 || T < 0 || H < 0 || N < 0 || !gate_ok(gate) || (backward != 0 && backward != 1))
+        return KLA_ERR_INVALID_ARG;
+    if (!dtype_ok(in_dtype)) return KLA_ERR_UNSUPPORTED_DTYPE;
+    Sizes s;
+    if (!sizes(B, T, H, N, gate, &s)) return KLA_ERR_INVALID_ARG;
+    *out = kla_gated_plan_t{};
+    if (s.n == 0) return KLA_OK;
+    alignas(16) static const float any[4] = {};  // only where it lies is looked at
+    const Launch l = backward ? plan_backward(B, T, H, N, in_dtype, gate, any, any, any, any, any)
+                              : plan_forward(B, T, H, N, in_dtype, gate, any, any, any);
+    out->tiles = l.tiles;
+    out->channels = 32 / l.S * l.vec;
+    out->parts = l.S;
+    out->tokens = tokens_of_lane(in_dtype, gate == KLA_GATE_HEAD && N > 1, backward, l.few);
+    out->warps = l.W;
+    out->cluster = l.C;
+    out->whole_rows = l.copy == WIDE;
+    const int64_t round = (int64_t)l.C * l.W * l.S * out->tokens;
+    out->rounds = (T + round - 1) / round;
+    return KLA_OK;
 }
 
 KLA_API kla_status_t kla_gated_scan_step(const void *f, const void *x, kla_dtype_t in_dtype, kla_gate_t gate,
@@ -378,9 +422,7 @@ KLA_API kla_status_t kla_gated_scan_backward(const void *f, kla_dtype_t in_dtype
     }
 
     const bool head = gate == KLA_GATE_HEAD && N > 1;
-    const Array arrays[5] = {{g_h, 4, true}, {grad_f ? h : nullptr, 4, true}, {grad_x, e, false},
-                             {f, e, true}, {grad_f, e, false}};
-    const Launch l = plan(B, T, H, N, arrays, head ? 3 : 5, Resident{in_dtype, head, true});
+    const Launch l = plan_backward(B, T, H, N, in_dtype, gate, f, h, g_h, grad_f, grad_x);
     if (l.tiles > kMaxGrid / l.C) return KLA_ERR_INVALID_ARG;
     const int64_t parts = head ? parts_of(N, 32 / l.S * l.vec) : 1;
     GatedBackwardParams prm;

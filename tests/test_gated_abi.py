@@ -145,3 +145,41 @@ def test_backward_of_heads_without_channels(lib):
     assert bwd(*args(1, None)) == 0
     assert bwd(*args(0, 2 * P)) == 0
     assert bwd(*args(1, 2 * P, N=4)) == 1        # channels, and no states or gradients given
+
+
+def test_plan_argument_errors(lib):
+    plan = lib.kla_gated_scan_plan
+    room = (ctypes.c_char * 64)()
+    args = lambda **kw: [kw.get("B", 1), kw.get("T", 8), kw.get("H", 2), kw.get("N", 4), kw.get("dt", 0),
+                         kw.get("gate", 0), kw.get("backward", 0), kw.get("out", room)]
+    assert plan(*args()) == 0
+    for bad in ("B", "T", "H", "N"):
+        assert plan(*args(**{bad: -1})) == 1
+    assert plan(*args(dt=2)) == 2
+    assert plan(*args(gate=2)) == 1
+    assert plan(*args(backward=2)) == 1
+    assert plan(*args(out=None)) == 1
+    assert plan(*args(B=1 << 40, T=1 << 40)) == 1
+    import kalman_linear_attention_b200 as kla
+    assert kla.gated_scan_plan(0, 8, 2, 4) == (0,) * 8
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_plan(dtype):
+    """Tiles cover the channels, rounds the tokens; rows that start on 16 bytes
+    are not cut shorter than a sector of memory in the inputs' type."""
+    import kalman_linear_attention_b200 as kla
+    rng = np.random.default_rng(0)
+    for _ in range(3000):
+        B, T, H = (int(2 ** rng.uniform(0, top)) for top in (7, 16, 6))
+        N = int(rng.choice([1, 8, 31, 64, 80, 128, int(2 ** rng.uniform(0, 9))]))
+        head, backward = bool(rng.integers(2)), bool(rng.integers(2))
+        p = kla.gated_scan_plan(B, T, H, N, dtype, head, backward)
+        what = (B, T, H, N, head, backward, p)
+        assert p.tiles * p.channels >= B * H * N, what
+        span = p.cluster * p.warps * p.parts * p.tokens
+        assert (p.rounds - 1) * span < T <= p.rounds * span, what
+        assert p.channels * p.parts == (64 if p.whole_rows else 32), what
+        assert 1 <= p.warps <= 16 and 1 <= p.cluster <= 8, what
+        if p.whole_rows and p.parts > 1:
+            assert p.channels * dtype.itemsize >= 32, what
