@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gated_gpu import reference, reference_backward
+from test_gated_gpu import PATHS, _runs, reference, reference_backward
 
 
 @pytest.fixture(scope="module")
@@ -183,3 +183,25 @@ def test_plan(dtype):
         assert 1 <= p.warps <= 16 and 1 <= p.cluster <= 8, what
         if p.whole_rows and p.parts > 1:
             assert p.channels * dtype.itemsize >= 32, what
+
+
+@pytest.mark.parametrize("gate", ["channel", "head"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_every_form_has_a_path(gate, dtype):
+    """No form that a plan can choose, of those that run long enough for several
+    rounds, is without a shape among the GPU tests' paths."""
+    import kalman_linear_attention_b200 as kla
+    kind = lambda p: (p.whole_rows, p.parts, "cluster" if p.cluster > 1 else "long" if p.warps > 8 else "alone")
+    rng = np.random.default_rng(1)
+    for backward in (False, True):
+        tested = set()
+        for path in PATHS:
+            p, right = _runs(path, dtype, gate, backward)
+            assert right, (path, p)
+            tested.add(kind(p))
+        for _ in range(20000):
+            B, T, H = (int(2 ** rng.uniform(0, top)) for top in (8, 16.2, 6))
+            N = int(rng.choice([2, 8, 16, 32, 64, 80, 128, 256, int(2 ** rng.uniform(1, 9))]))
+            p = kla.gated_scan_plan(B, T, H, N, dtype, gate == "head", backward)
+            if p.rounds >= 3:
+                assert kind(p) in tested, (B, T, H, N, p)

@@ -487,3 +487,88 @@ def test_offsets_past_32_bits_of_rows_off_16_bytes(gate):
     want = reference_backward(_np(f[sl]), _np(h[sl]), _np(h[sl]), _np(h[:, -41]), HALF_STEP[torch.bfloat16])
     assert_within(gx[sl], *want["x"], "last gradients of x")
     assert_within(gf[sl], *want["f"], "last gradients of f")
+
+
+# Every form of the kernels over several rounds: how a tile runs (a CTA alone, a
+# cluster, a CTA with more than 8 warps), parts of a warp, rows that start on 16
+# bytes or not, B, T, H, N (on 148 multiprocessors)
+PATHS = [("alone", 1, True, (8, 700, 16, 128)), ("alone", 2, True, (1, 1200, 40, 128)),
+         ("alone", 4, True, (1, 2400, 16, 128)), ("alone", 8, True, (1, 4200, 8, 128)),
+         ("alone", 1, False, (10, 700, 23, 31)), ("alone", 2, False, (6, 1200, 23, 31)),
+         ("alone", 4, False, (3, 2400, 23, 31)), ("cluster", 8, True, (1, 17000, 2, 64)),
+         ("cluster", 8, True, (1, 9000, 11, 64)), ("cluster", 8, True, (1, 17000, 4, 128)),
+         ("cluster", 4, False, (1, 17000, 3, 11)), ("long", 1, True, (1, 8300, 60, 128)),
+         ("long", 2, True, (1, 16500, 30, 128)), ("long", 4, True, (1, 33000, 15, 128)),
+         ("long", 8, True, (1, 66000, 8, 120)), ("long", 4, False, (1, 33000, 9, 101))]
+
+
+def _runs(path, dtype, gate, backward):
+    """The plan of a path, and whether it is the one that the path is there for."""
+    kind, parts, whole, shape = path
+    if dtype == torch.bfloat16 and parts == 8:  # rows of 16 bytes: 4 parts, and half the tiles
+        kind, parts = "cluster", 4
+    if kind == "long" and whole and gate == "head" and backward:  # 8 warps have 64 KB
+        kind = "alone"
+    p = _kla().gated_scan_plan(*shape, dtype, gate == "head", backward)
+    ran = "cluster" if p.cluster > 1 else "long" if p.warps > 8 else "alone"
+    return p, (ran, p.parts, p.whole_rows) == (kind, parts, whole) and p.rounds >= 3
+
+
+def _walk(f, x):
+    """x_t += f_t x_{t-1} in place, token after token."""
+    steps = list(zip(f.unbind(1), x.unbind(1)))
+    for (_, last), (gate, now) in zip(steps, steps[1:]):
+        now.addcmul_(gate, last)
+    return x
+
+
+def reference_on_device(f, x, h0):
+    """reference() by torch in fp64 on the device: the states with their
+    magnitudes beside them, then the bound."""
+    f = f.double() if f.dim() == 4 else f.double()[..., None]
+    both = torch.stack([x, x.abs()], 2).double()
+    gates = torch.stack([f, f.abs()], 2)
+    if h0 is not None:
+        both[:, 0] += gates[:, 0] * torch.stack([h0, h0.abs()], 1).double()
+    h, mag = _walk(gates, both).unbind(2)
+    return h, _walk(f.abs(), 4 * U * mag)
+
+
+def assert_near(got, ref, bound, what):
+    bad = ~((got.double() - ref).abs() <= bound)
+    n = int(bad.sum())
+    assert n == 0, f"{what}: {n} of {bad.numel()} values off, the first at {bad.nonzero()[0].tolist()}"
+
+
+@pytest.mark.parametrize("path", PATHS, ids=lambda p: f"{p[0]}-{p[1]}-{'whole' if p[2] else 'any'}-"
+                                                      + "x".join(map(str, p[3])))
+@pytest.mark.parametrize("gate", ["channel", "head"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_every_path(path, gate, dtype):
+    """The form that a shape is there for is the one that runs, and every
+    element is within the bounds of the formulas."""
+    kla = _kla()
+    for backward in (False, True):
+        p, right = _runs(path, dtype, gate, backward)
+        assert right, (p, "backward" if backward else "forward")
+    B, T, H, N = path[3]
+    gen = torch.Generator(device=DEV).manual_seed(31)
+    randn = lambda *s: torch.randn(s, generator=gen, device=DEV)
+    f = torch.sigmoid(2 * randn(B, T, H, *((N,) if gate == "channel" else ())) + 2).to(dtype)
+    x, g, h0 = randn(B, T, H, N).to(dtype), randn(B, T, H, N), randn(B, H, N)
+    h = kla.gated_scan_forward(f, x, h0)
+    assert_near(h, *reference_on_device(f, x, h0), "h")
+    gf, gx, gh0 = kla.gated_scan_backward(f, h, g, h0)
+    half = HALF_STEP[dtype]
+    later = torch.cat([f[:, 1:], torch.zeros_like(f[:, :1])], 1).flip(1)
+    E, eE = (t.flip(1) for t in reference_on_device(later, g.flip(1), None))
+    assert_near(gx, E, eE + half * (E.abs() + eE), "gradient of x")
+    before = torch.cat([h0[:, None], h[:, :-1]], 1).double()
+    terms, off = E * before, before.abs() * eE
+    off += U * terms.abs()
+    if gate == "head":
+        off = off.sum(-1) + (8 + N / 32) * U * terms.abs().sum(-1)
+        terms = terms.sum(-1)
+    assert_near(gf, terms, off + half * (terms.abs() + off), "gradient of f")
+    first = f[:, 0].double() if gate == "channel" else f[:, 0].double()[..., None]
+    assert_near(gh0, first * E[:, 0], first.abs() * eE[:, 0] + U * (first * E[:, 0]).abs(), "gradient of h0")
