@@ -414,3 +414,45 @@ def test_gradients_that_are_not_formed_are_refused(name):
             call().sum().backward()
         with torch.no_grad():  # none is wanted
             assert call().shape == x.shape
+
+
+# Warps that go through several tokens and shares of their heads, so that ring
+# and table are used again: every width of vectors and number of units a lane,
+# rows that do not fill their lanes, both tensors uneven
+MANY = [(4, 2000, 32, 8, 128, 128), (2, 6001, 12, 3, 16, 16), (1, 9001, 5, 1, 80, 32), (2, 5000, 7, 2, 250, 100),
+        (3, 2500, 17, 1, 96, 64), (1, 4001, 3, 1, 1024, 1024), (1, 4003, 2, 1, 1023, 510), (1, 5001, 3, 2, 126, 126),
+        (1, 4007, 2, 2, 500, 0), (30, 1100, 4, 4, 8, 6)]
+
+
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("interleaved", [False, True], ids=["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_many_tokens(shape, interleaved, dtype):
+    kla = _kla()
+    B, T, Hq, Hk, D, rot = shape
+    gen = torch.Generator(device=DEV).manual_seed(14)
+    randn = lambda *s: torch.randn(s, generator=gen, device=DEV)
+    x = {"q": (2 * randn(B, T, Hq, D)).to(dtype), "k": randn(B, T, Hk, D).to(dtype),
+         "gq": randn(B, T, Hq, D).to(dtype), "gk": randn(B, T, Hk, D).to(dtype), "wq": 1 + 0.2 * randn(D),
+         "wk": 1 + 0.2 * randn(D)}
+    freq = frequencies(rot).to(DEV) if rot else None
+    positions = torch.randint(0, 1 << 20, (B, T), generator=gen, device=DEV) if rot else None
+    angle = angles(positions, freq)
+    rotation = dict(inv_freq=freq, positions=positions, interleaved=interleaved, eps=1e-5)
+    got = kla.qk_norm_rotary_forward(x["q"], x["k"], x["wq"], x["wk"], **rotation)
+    grads = kla.qk_norm_rotary_backward(x["q"], x["k"], x["gq"], x["gk"], x["wq"], x["wk"], **rotation)
+
+    def near(got, value, error, what):
+        bad = ~((got.double() - value).abs() <= error)
+        assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, the first at {bad.nonzero()[0].tolist()}"
+
+    for name, y, gx, gw in (("q", got[0], grads[0], grads[2]), ("k", got[1], grads[1], grads[3])):
+        at = (double(x["w" + name]), 1e-5, angle, rot, interleaved, 1.0)
+        near(y, *rounded(*reference(double(x[name]), *at), dtype), name)
+        dx, edx, dw, edw = reference_backward(double(x[name]), double(x["g" + name]), *at)
+        near(gx, *rounded(dx, edx, dtype), "gradient of " + name)
+        near(gw, dw, edw, "gradient of the weight of " + name)
+    if rot:
+        turned = kla.rotary_forward(x["q"], freq, positions, interleaved=interleaved)
+        zero = torch.zeros_like(x["q"], dtype=torch.float64)
+        near(turned, *rounded(*turn(double(x["q"]), zero, angle, rot, interleaved, 1.0), dtype), "rotary")
