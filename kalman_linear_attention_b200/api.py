@@ -796,7 +796,9 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "n
       times slower and the fastest keeps its angle;
     * ``"yarn"``: pairs that make more than ``fast`` turns over ``length`` keep
       their angle, those with fewer than ``slow`` are divided by ``factor``,
-      with a linear ramp over the turns between; scale = 0.1 ln(factor) + 1.
+      with a ramp between that is linear in the turns, as published; scale = 0.1
+      ln(factor) + 1.  A checkpoint whose ramp is linear in the pair's index
+      instead needs frequencies of its own.
     """
     if rot_dim < 0 or rot_dim % 2:
         raise ValueError("rot_dim must be even and not negative")

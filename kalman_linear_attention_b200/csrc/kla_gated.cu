@@ -26,15 +26,18 @@ bool sizes(int64_t B, int64_t T, int64_t H, int64_t N, kla_gate_t gate, Sizes *s
     return true;
 }
 
-// Tokens of a lane in a round: as many as make 4 to 8 KB of a warp's rows in
-// flight (two channels a lane).  Forward, half as many: the long fp32 shape
-// (B=1, T=65536, 32 x 128) 580 us against 659 with 16 tokens; shared gates
-// 456 us with 16 against 508 with 8.  bf16 gates of each channel: where an SM
-// has one CTA at most (`few`: no more tiles than SMs), T=32768, 32 x 128, 195 us
-// with 16, 204 with 12; where it has more, B=8, T=2048, 16 x 128, 49.6 us with
-// 12, 51.5 with 16.  Backward: B=8, T=2048, 16 x 128 fp32 108 us against 124
-// with 8; bf16 80 us with 8 against 85 with 4; shared gates, the long fp32
-// shape, 822 us with 16 against 910 with 8.
+// Tokens of a lane in a round: 2 KB (bf16, shared gates, forward) to 8 KB (shared
+// gates, backward) of a warp's rows in flight, two channels a lane.  Measured
+// beside the other choice, on the long shape (B=1, T=65536, 32 x 128) and an
+// ordinary one (B=8, T=2048, 16 x 128):
+//   shared gates, forward   fp32 long 382 us, 494 with 8; bf16 ordinary 42, 50;
+//                 backward  619, 711; 64, 72
+//   fp32, forward           ordinary 67, 73 with 16; long 526, 487
+//         backward          107, 123 with 8; 947, 848
+//   bf16, forward, where an SM has one CTA at most (`few`: no more tiles than
+//         SMs)              T=32768, 32 x 128, 189, 199 with 12
+//         where it has more ordinary 49.7, 52.6 with 16
+//         backward          ordinary 79.7, 82.4 with 4
 template <typename Tin, bool HEAD, bool BACKWARD>
 constexpr int tokens_of_lane(bool few) {
     if (HEAD) return 16;
@@ -114,12 +117,16 @@ struct Resident {
     }
 };
 
-// The widest tiles of which there are enough: 0.8 of the SMs (shared gates,
-// the long fp32 shape: 128 tiles of 32 channels 424 us, 256 of 16 455; B=2, T=5001,
-// 12 x 80, 21 us against 27), or 1.5 of them with one channel a lane.  Rows that start
-// on 16 bytes, and on pairs of channels in every array, take two channels a
-// lane (half the instructions for a channel, and two chains of multiply-adds
-// side by side), others one; a warp's lanes in 1, 2, 4 or (fp32) 8 parts.
+// The widest tiles of which there are enough: 0.8 of the SMs, or 1.5 of them
+// with one channel a lane.  Measured, forward and backward: shared gates, the
+// long fp32 shape, 128 tiles of 32 channels 380 and 616 us, 256 of 16 440 and 904;
+// B=2, T=5001, 12 x 80, 120 tiles 21 and 37, 240 27 and 51.  Near the edge, fp32,
+// T=4096, 112 tiles of 64 channels 63 and 109, as 224 of 32 59 and 102 (shared
+// gates 51 and 72, 43 and 78); 120 tiles 64 and 111, as 240 64 and 107 (53 and 72,
+// 48 and 76).  Rows that start on 16 bytes, and on pairs of channels in every
+// array, take two channels a lane (half the instructions for a channel, and two
+// chains of multiply-adds side by side), others one; a warp's lanes in 1, 2, 4 or
+// (fp32) 8 parts.
 template <typename F>
 Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, const Array *arrays, int n, const F &resident) {
     Launch l;
@@ -156,13 +163,15 @@ Launch plan(int64_t B, int64_t T, int64_t H, int64_t N, const Array *arrays, int
     // with 6; fp32 66, 74 and 64; shared gates 42, 41 and 47)
     l.W = (int)std::min({(int64_t)8, held, chunks});
     if (3 * l.tiles <= 2 * sms) {
-        // few tiles all the same: clusters, until there are two CTAs for each SM
+        // few tiles all the same: clusters, until there are more CTAs than SMs
         while (l.C < kGatedMaxCluster && l.tiles * l.C <= sms && (int64_t)l.C * l.W < chunks) l.C *= 2;
     } else if (l.few && chunks >= 32 * kGatedMaxWarps) {
         // one CTA an SM, and a long sequence: as many warps as have 64 KB of
-        // rows in a round (the long fp32 shape: 515 us with 16 against 608
-        // with 8; backward 922 against 1132; for 16 chunks a warp, B=1,
-        // T=16384, 16 x 128 in bf16, 74 us against 58)
+        // rows in a round (the long fp32 shape: 512 us with 16 against 602
+        // with 8, backward 932 against 1123; shared gates 397 against 422; T=32768
+        // in bf16 197 against 206).  B=1, 16 x 128 in bf16, four parts: of 256
+        // chunks 74 us with 16, 58 with 8, of 384 105 and 84; above the limit
+        // 512 137 and 111, backward 179 and 183
         l.W = (int)std::max<int64_t>(
             l.W, std::min({(int64_t)kGatedMaxWarps, held, 64 * 1024 / resident.stage(l)}));
     }

@@ -30,7 +30,7 @@
 //      stores the states straight from registers.
 //
 // With few channels the sequence itself has to fill the GPU: a cluster of C
-// CTAs then shares the tile, its ranks taking consecutive spans of W x L
+// CTAs then shares the tile, its ranks taking consecutive spans of W x S x L
 // tokens; each rank writes its span's composed pair into every rank's shared
 // memory, and one cluster barrier a round replaces any hand-over through
 // global memory: no workspace, no flags, no waiting loops, one launch, and
@@ -42,9 +42,9 @@
 // on rows of f and h that are shifted by one token against g.
 //
 // Every element is read and written once: HBM is the floor.  Copies reach 6.46
-// TB/s; the scan of B=1, T=65536, 32 x 128 in fp32 takes 500 to 535 us (0.93 to
-// 0.99 of that), its backward pass 900 to 950 (0.87 to 0.92), the bf16 scan of
-// B=8, T=2048, 16 x 128 49.6 us (0.84) and 79 backward (0.91).  What bounds the
+// TB/s; the scan of B=1, T=65536, 32 x 128 in fp32 takes 510 to 535 us (0.93 to
+// 0.98 of that), its backward pass 930 to 950 (0.88 to 0.89), the bf16 scan of
+// B=8, T=2048, 16 x 128 49.7 us (0.84) and 79.5 backward (0.91).  What bounds the
 // rest is the chain of rounds, whose copies, barrier and exchange the 8 warps
 // of a lone CTA do not hide (B=2, T=5001, 12 x 80, shared gates, 120 tiles: 10
 // rounds of 1.6 us, 21 us forward and 37 backward, 0.58 and 0.49).
